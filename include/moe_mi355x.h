@@ -55,14 +55,15 @@ typedef enum {
 } moe_status;
 
 typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 } moe_dtype;
-typedef enum { MOE_WF_DENSE = 0, MOE_WF_AFFINE_Q4 = 1, MOE_WF_AFFINE_Q8 = 2 } moe_wformat;
+/* (the value 3 is not assigned) */
+typedef enum { MOE_WF_DENSE = 0, MOE_WF_AFFINE_Q4 = 1, MOE_WF_AFFINE_Q8 = 2, MOE_WF_FP8 = 4 } moe_wformat;
 typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_GEGLU = 1 } moe_activation;
 
 /*
  * Layer shape and format.
  *  d_model, d_ff  > 0; for the affine formats multiples of 64 and of
  *                 group_size (the groups run along both reduction dims);
- *                 multiples of 8 otherwise.
+ *                 multiples of 16 for MOE_WF_FP8, of 8 otherwise.
  *  n_experts      routed experts E, 1..1024.
  *  top_k          1..min(32, n_experts).
  *  n_shared       always-on shared experts (weight 1.0, not renormalised), 0..8;
@@ -75,6 +76,9 @@ typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_GEGLU = 1 } moe_activation;
  *                 kernel", "Multi-bit handling"; DS4Server #112, "Native
  *                 implementation scope") need a 16-bit act_dtype (bf16 or
  *                 fp16); their scales and biases are in that dtype.
+ *                 MOE_WF_FP8: e4m3 codes with one fp32 scale per 128 x 128
+ *                 block, any act_dtype; the products are of 8-bit codes on
+ *                 both sides (see "8-bit floating point" below).
  *  group_size     affine group length along the reduction dim: 32, 64 or 128.
  *  gate_up_fused  1: one [2*d_ff][d_model] matrix per expert whose rows are
  *                 [gate | up]; 0: separate gate and up matrices.
@@ -110,6 +114,8 @@ typedef struct {
  *         scale*q + bias of its group ("affine" quantisation with 16-bit scales
  *         and biases: "SwitchGLU: grouped-expert Metal kernels"
  *         (ml-explore/mlx-lm #2044), "When it applies").
+ *  fp8:   w = uint8 [E+S][N][K] e4m3 codes; scales = fp32
+ *         [E+S][ceil(N/128)][ceil(K/128)]; biases = w_packed = NULL.
  * gate, up: N = d_ff, K = d_model; gate_up: N = 2*d_ff, K = d_model;
  * down: N = d_model, K = d_ff.
  */
@@ -358,6 +364,77 @@ int moe_forward_noalloc(const moe_layer_desc *desc, int32_t T, const void *x,
  * MOE_E_HIP if the launch fails.
  */
 int moe_stream_read(const void *src, size_t bytes, uint32_t *out, int32_t blocks, void *stream);
+
+/*
+ * ---- 8-bit floating point ---------------------------------------------------
+ *
+ * Codes are OCP e4m3 (4 significant bits, largest value 448, no infinities).
+ * A block of values has one fp32 scale: with m = max(amax, 448 * 2^-126),
+ * amax the largest magnitude of the block (NaNs aside),
+ *   scale = m / 448,   code = e4m3(448 * x / m), rounded to nearest even,
+ * and a code stands for scale * code.  The product 448 * x and the quotient
+ * are each rounded to fp32 first; for inputs of up to 21 significant bits
+ * (bf16, fp16) the first is exact and a value exactly between two codes goes
+ * to the even one.  A NaN has the code of a NaN; a block with an infinity has
+ * an infinite scale, its finite values code 0 and its infinities a NaN code.
+ * Blocks are 128 consecutive reduction elements of one row (activations), or
+ * 128 rows of them (weights); the last block of a dimension may be shorter.
+ *
+ * moe_fp8_quantize: the codes of x, n_matrices arrays [rows][cols] of `dtype`
+ * (a moe_dtype), as codes[n_matrices][rows][cols].  block_rows = 1: one scale
+ * per row and 128 columns, scales[ceil(cols/128)][n_matrices * rows] (the
+ * scales of one column block for consecutive rows are contiguous);
+ * block_rows = 128: one per 128 x 128 block, scales[n_matrices]
+ * [ceil(rows/128)][ceil(cols/128)], the layout of moe_proj.  cols is a
+ * positive multiple of 16.  A zero n_matrices or rows enqueues nothing.
+ * MOE_E_INVALID for a bad size, dtype, block_rows or pointer, or for more
+ * than 2^24 - 1 workgroups (32 rows x 128 columns, or one block, each).
+ */
+int moe_fp8_quantize(int32_t n_matrices, int32_t rows, int32_t cols, const void *x, int32_t dtype,
+                     int32_t block_rows, uint8_t *codes, float *scales, void *stream);
+
+/*
+ * Grouped product of 8-bit codes: for output row p < rows, in the range
+ * expert_off[e] <= p < expert_off[e+1] of expert e, and r = row_map[p],
+ *   y[p][n] = sum_b a_scales[b][r] * w_scales[e][n/128][b]
+ *                   * sum_{k in block b} a[r][k] * w[e][n][k],
+ * the running sum in fp32, y rounded once to out_dtype.  The inner sums are
+ * in fp32 too when out_dtype is fp32 or the experts have few rows; else they
+ * may be those of the 8-bit matrix instruction, which drops from a product
+ * what lies 13 binary places below the largest of its 8 neighbours.
+ * a: codes [a_rows][K] with a_scales [ceil(K/128)][a_rows] (moe_fp8_quantize,
+ * block_rows 1); w: codes [n_experts][N][K] with w_scales
+ * [n_experts][ceil(N/128)][ceil(K/128)] (block_rows 128); row_map and
+ * expert_off as moe_dispatch writes them.  row_map may be NULL (r = p,
+ * a_rows >= rows); expert_off may be NULL when n_experts is 1 (all rows): an
+ * ordinary product a w^T.  N and K are positive multiples of 16,
+ * N * K <= 2^31, 1 <= n_experts <= 1024.  Rows past expert_off[n_experts] are
+ * left as they are.  Offsets are read as if clamped to [0, rows] (each range
+ * starting at its own offset); a row_map entry outside [0, a_rows) gives a
+ * row of zeros.  rows == 0 enqueues nothing.  MOE_E_INVALID for a bad size,
+ * dtype or pointer.
+ *
+ * Backward: with respect to the activations it is the same product with the
+ * transposed weights, whose square blocks keep their scales:
+ * moe_fp8_transpose writes wt[n_matrices][K][N] and wt_scales
+ * [n_matrices][ceil(K/128)][ceil(N/128)] from w [n_matrices][N][K] (N and K
+ * positive multiples of 16), an exact copy to keep while w does not change.
+ */
+int moe_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_t a_rows, const uint8_t *a,
+                   const float *a_scales, const int32_t *row_map, const int32_t *expert_off, const uint8_t *w,
+                   const float *w_scales, void *y, int32_t out_dtype, void *stream);
+int moe_fp8_transpose(int32_t n_matrices, int32_t N, int32_t K, const uint8_t *w, const float *w_scales,
+                      uint8_t *wt, float *wt_scales, void *stream);
+
+/*
+ * An MOE_WF_FP8 layer runs through moe_expert_ffn, moe_forward (and its
+ * _timed and _noalloc forms) and moe_backward like any other: x is quantised
+ * per token and 128 columns, gate and up are products of codes, the gated
+ * unit h (fp32, or rounded per operation when glu_round is set) is quantised
+ * per row and 128 columns, down is a product of codes with fp32 results.
+ * moe_backward differentiates the layer with the weights' values
+ * (scale * code) and the activations unrounded.
+ */
 
 /* A static, human-readable name of a moe_status value. */
 const char *moe_status_string(int status);

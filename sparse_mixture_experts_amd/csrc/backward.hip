@@ -13,7 +13,8 @@
 //   dx_t = sum of its slots' dx_r in slot order + shared rows + W_r dl, with
 //   dl the softmax backward of the slot weights from dw            (kernel 5)
 // The forward's per-op rounding is not differentiated (the unrounded GLU).
-// fp32 layers run kernels 1-4 here, all arithmetic fp32 on the vector units
+// fp32 and fp8 layers run kernels 1-4 here (fp8 weights as scale * code, x as
+// it is: the rounding to codes is not differentiated either), all arithmetic fp32 on the vector units
 // (each weight element is read where its row or column is reduced, for up to
 // kMR routed rows at a time); 16-bit layers run the matrix-core versions of
 // kernels 1-4 (backward_mfma.hip).  Kernel 5 serves both.
@@ -30,6 +31,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMR = 8;  // routed rows per pass
 
+constexpr int kFp8Codes = -8;
+
 // One projection of every expert: N weight rows of K columns each (rows
 // `row_off` .. of the stored [nre][K] matrix of an expert).
 struct WView {
@@ -39,7 +42,7 @@ struct WView {
 };
 struct WFormat {
   int act_dtype;  // moe_dtype of dense weights and of scales/biases
-  int bits;       // 0: dense; 4 or 8: affine codes
+  int bits;       // 0: dense; 4 or 8: affine codes; kFp8Codes: e4m3 codes with fp32 scales per 128 x 128
   int group;
 };
 
@@ -51,6 +54,12 @@ __device__ __forceinline__ float wload(const WFormat &f, const WView &v, int e, 
     if (f.act_dtype == MOE_DT_F32) return static_cast<const float *>(v.w)[i];
     const uint32_t h = static_cast<const uint16_t *>(v.w)[i];
     return f.act_dtype == MOE_DT_F16 ? f16_bits_to_f32(h) : bf16_bits_to_f32(h);
+  }
+  if (f.bits == kFp8Codes) {
+    const int nbr = (v.nre + 127) / 128, nbk = (v.K + 127) / 128;
+    const float s = static_cast<const float *>(static_cast<const void *>(
+        v.sc))[(int64_t(e) * nbr + (v.row_off + n) / 128) * nbk + k / 128];
+    return s * __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t *>(v.w)[row * v.K + k], 0);
   }
   const int per = 32 / f.bits;
   const uint32_t word = static_cast<const uint32_t *>(v.w)[row * (v.K / per) + k / per];
@@ -342,7 +351,7 @@ void launch_backward(const moe_layer_desc *d, int32_t T, const void *x, const mo
   const int N = T * K, R = N + S * T;
   const int max_items = std::min(E, N) + S;
   const bool fused = d->gate_up_fused;
-  const int bits = d->w_format == MOE_WF_AFFINE_Q8 ? 8 : d->w_format == MOE_WF_AFFINE_Q4 ? 4 : 0;
+  const int bits = d->w_format == MOE_WF_AFFINE_Q8 ? 8 : d->w_format == MOE_WF_AFFINE_Q4 ? 4 : fp8(d) ? kFp8Codes : 0;
   const moe_proj &pg = fused ? w->gate_up : w->gate, &pu = fused ? w->gate_up : w->up;
   auto view = [&](const moe_proj &p, int n, int k, int row_off, int nre) {
     return WView{p.w, static_cast<const uint16_t *>(p.scales), static_cast<const uint16_t *>(p.biases), n, k,

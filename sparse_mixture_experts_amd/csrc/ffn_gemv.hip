@@ -236,6 +236,10 @@ void launch_expert_ffn(const moe_layer_desc *d, int32_t T, const void *x, const 
                        const moe_weights *w, const int32_t *counters, const PlanItem *act_items,
                        const PlanItem *tiles, int64_t max_tiles, const FfnScratch &sc, void *ys,
                        int8_t *ys_sh, void *stream, StageMarker *mk, int down_parts) {
+  if (fp8(d)) {
+    launch_expert_ffn_fp8(d, T, x, row_map, w, counters, tiles, sc, static_cast<float *>(ys), stream, mk);
+    return;
+  }
   if (use_mfma(d)) {
     launch_expert_ffn_mfma(d, T, x, row_map, w, counters, tiles, max_tiles, sc, ys, ys_sh, stream, mk,
                            down_parts);

@@ -1392,8 +1392,8 @@ void launch_decode(const DecArgs &da, int qb, int64_t max_tiles, hipStream_t s) 
 bool use_mfma(const moe_layer_desc *d) {
   // 16-bit activations with every reduction length a whole number of
   // 64-element groups; fp32 layers and other shapes take the dequant-GEMV
-  // kernels.
-  return d->act_dtype != MOE_DT_F32 && d->d_model % 64 == 0 && d->d_ff % 64 == 0;
+  // kernels; fp8 layers have kernels of their own.
+  return !fp8(d) && d->act_dtype != MOE_DT_F32 && d->d_model % 64 == 0 && d->d_ff % 64 == 0;
 }
 
 // Experts with two or more row tiles on average: the work runs in groups of
@@ -1452,6 +1452,7 @@ int plan_tile_rows(const moe_layer_desc *d, int32_t T) {
   // Decode-sized groups (T*k/E <= 8 rows per expert on average, the pages'
   // small-group regime) use 16-row tiles; larger groups 64-row tiles.
   const int64_t N = int64_t(T) * d->top_k;
+  if (fp8(d)) return fp8_tile_rows(N, d->n_experts, true);
   return N <= 8LL * d->n_experts ? 16 : 64;
 }
 

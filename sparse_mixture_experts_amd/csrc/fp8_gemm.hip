@@ -1,0 +1,646 @@
+// fp8_gemm.hip -- products of e4m3 codes with one fp32 scale per 128
+// reduction elements (activations: per row; weights: per 128 x 128 block),
+// grouped by expert:
+//   y[p][n] = sum_b sa[b][r] sw[e][n / 128][b] sum_{k in block b} a[r][k] w[e][n][k],
+// r = row_map[p] (or p), e the expert whose range of rows holds p.
+//
+// The sum over one block is one v_mfma_f32_16x16x128_f8f6f4 or four
+// v_mfma_f32_16x16x32_f16 (fp8_common.h), started from zero, whose four
+// results per lane one fma each brings to the running fp32 sum with the
+// block's scale: 16 vector cycles beside 32 or 64 matrix cycles.  Operand a holds 16 weight rows n and operand b 16 token rows, so a lane's
+// results are 4 consecutive outputs of one token and its scale is one value.
+// Lane group g = lane / 16 holds bytes 16 g .. +15 and 64 + 16 g .. +15 of the
+// 128 (of both operands), so each 16-byte load of a wave covers whole 64-byte
+// pieces of 16 rows.
+//
+// Two kernels.  The tile kernel (experts with many rows) takes 64 or 128
+// token rows by 256 weight rows: the rows' codes go through LDS, double
+// buffered, the weights straight from memory to the registers of the one wave
+// that uses them, a block ahead.  The decode kernel (few rows per expert) is
+// bound by the weights' bytes: the waves of a workgroup split the reduction,
+// each with several blocks of weights in flight, and add up through LDS.
+#include <algorithm>
+
+#include "fp8_common.h"
+#include "launch.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kNW = kThreads / kWave;
+constexpr int kNT = 4;                    // 16-row weight tiles per wave of the tile kernel
+constexpr int kBN = kNW * kNT * 16;       // weight rows per workgroup (256)
+constexpr int kRowBytes = kFp8Block + 16; // LDS row: 16 rows' 16-byte pieces fall into 16 different bank groups
+constexpr int kPieces = kFp8Block / 16;   // 16-byte pieces per row and block (8)
+
+// What a projection writes: the product, or the gated unit of two of them
+// (as e4m3 codes per 128 columns from the tile kernel, as fp32 from the
+// decode kernel).
+constexpr int kPlain = 0, kGated = 1;
+// Activations of the decode kernel: codes with scales, or values that it
+// quantises itself (their block maxima are four lanes' work).
+constexpr int kSrcCodes = 3;  // else a moe_dtype
+
+struct Fp8Args {
+  const void *a;             // codes [a_rows][K], or values [a_rows][K] (decode kernel)
+  const float *as;           // [blocks][a_rows]
+  int64_t a_rows;
+  const int32_t *row_map;    // null: row p is p
+  int rows, N, K;            // output rows, output columns, reduction
+  int T, n_routed;           // layer: rows past n_routed are shared experts' (token (p - n_routed) % T)
+  const uint8_t *w0, *w1;    // [E][N][K]; gated: gate (or [gate | up]) and up
+  const float *s0, *s1;      // [E][ceil(N/128)][ceil(K/128)]
+  int fused;                 // gated: w0 holds [gate | up]
+  int round, geglu;          // gated: per-op rounding mode, tanh-GELU gate
+  int E;
+  const int32_t *expert_off; // null: one expert has all rows
+  const PlanItem *tiles;     // layer: the work plan (expert_off unused)
+  const int32_t *counters;
+  void *out;                 // plain: [rows][N] out_dtype; gated: h (codes or fp32) [rows][N]
+  int out_dtype;
+  float *hs;                 // gated tile kernel: h scales [ceil(N/128)][rows]
+};
+
+// Tile `id` of BM rows over the experts' row ranges, and the number of tiles.
+// Ranges are clamped to [0, rows]; every lane of the wave takes part.
+__device__ __forceinline__ bool find_tile(const Fp8Args &a, int bm, int id, PlanItem &t, int &total) {
+  const int lane = lane_id();
+  const int per = (a.E + kWave - 1) / kWave;
+  const int e0 = lane * per, e1 = min(e0 + per, a.E);
+  auto range = [&](int e, int &lo, int &hi) {
+    lo = min(max(a.expert_off[e], 0), a.rows);
+    hi = min(max(a.expert_off[e + 1], lo), a.rows);
+  };
+  int n = 0;
+  for (int e = e0; e < e1; ++e) {
+    int lo, hi;
+    range(e, lo, hi);
+    n += (hi - lo + bm - 1) / bm;
+  }
+  const int incl = wave_incl_scan(n);
+  total = read_lane_i(incl, kWave - 1);
+  if (id >= total) return false;
+  int at = incl - n, fe = 0, frow = 0, frows = 0;
+  if (id >= at && id < incl) {
+    for (int e = e0; e < e1; ++e) {
+      int lo, hi;
+      range(e, lo, hi);
+      const int k = (hi - lo + bm - 1) / bm;
+      if (id < at + k) {
+        fe = e;
+        frow = lo + (id - at) * bm;
+        frows = min(bm, hi - frow);
+        break;
+      }
+      at += k;
+    }
+  }
+  const int src = __builtin_ctzll(__ballot(incl > id));
+  t.expert = read_lane_i(fe, src);
+  t.row0 = read_lane_i(frow, src);
+  t.rows = read_lane_i(frows, src);
+  return true;
+}
+
+// Number of row tiles of this call.
+__device__ __forceinline__ int count_tiles(const Fp8Args &a, int bm) {
+  if (a.tiles) return a.counters[1];
+  if (!a.expert_off) return (a.rows + bm - 1) / bm;
+  PlanItem t;
+  int total;
+  find_tile(a, bm, 0x7fffffff, t, total);
+  return total;
+}
+
+// This workgroup's row tile and column block (false: none is left).  Each
+// XCD takes one contiguous range of the work, ordered in groups of 8 column
+// blocks with the tiles of an expert together, so that what neighbours share
+// (a tile's rows, an expert's weights) is read into one L2.
+__device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanItem &t, int &bx) {
+  const int n_tiles = count_tiles(a, bm);
+  const int work = n_tiles * nbx;  // the grid has at least as many workgroups
+  const int lin = int(blockIdx.x);
+  if (lin >= work) return false;
+  int tile;
+  item_tile_block(xcd_contiguous(lin, work), n_tiles, nbx, min(nbx, kColGroup), tile, bx);
+  if (a.tiles) {
+    t = a.tiles[tile];
+  } else if (a.expert_off) {
+    int total;
+    find_tile(a, bm, tile, t, total);
+  } else {
+    t.expert = 0;
+    t.row0 = tile * bm;
+    t.rows = min(bm, a.rows - t.row0);
+  }
+  t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+  t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  return true;
+}
+
+// Source row of output row p, or -1 when the map points outside.
+__device__ __forceinline__ int source_row(const Fp8Args &a, int p) {
+  int r = p;
+  if (a.T && p >= a.n_routed) r = (p - a.n_routed) % a.T;
+  else if (a.row_map) r = a.row_map[p];
+  return unsigned(r) < unsigned(a.a_rows) ? r : -1;
+}
+
+__device__ __forceinline__ uint4 keep(const uint4 &v, bool ok) {
+  return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
+}
+
+// Four consecutive outputs of one row.
+__device__ __forceinline__ void store4(const Fp8Args &a, int64_t at, const fp8_acc &v) {
+  if (a.out_dtype == MOE_DT_F32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = a.out_dtype == MOE_DT_F16 ? f32_to_f16_bits(v[i]) : f32_to_bf16_bits(v[i]);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+        make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  }
+}
+
+// RB: 16-row blocks of token rows per tile.  EXACT: see Fp8Operand.
+template <int RB, int MODE, bool EXACT>
+__device__ __forceinline__ void tile_body(const Fp8Args &a) {
+  constexpr int BM = RB * 16;
+  constexpr int PPT = BM * kPieces / kThreads;      // 16-byte pieces of the rows per thread
+  constexpr int NTH = MODE == kGated ? kNT / 2 : kNT;
+  constexpr int COLS = kNW * NTH * 16;              // output columns per workgroup
+  // weight scale blocks that a workgroup meets: 256 rows cover two; gated:
+  // one of gate rows, and two of up rows when they start inside a block
+  constexpr int NS = MODE == kGated ? 3 : 2;
+  constexpr int SPT = (BM * NS + kThreads - 1) / kThreads;
+  __shared__ __align__(16) uint8_t sa[2][BM][kRowBytes];
+  __shared__ float ss[2][NS][BM];                   // row scale * weight scale
+  __shared__ float rmax[MODE == kGated ? kNW : 1][BM];
+
+  const int nbx = (a.N + COLS - 1) / COLS;
+  PlanItem tile;
+  int bx;
+  if (!my_work(a, BM, nbx, tile, bx)) return;
+  const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
+  const int lr = lane & 15, lg = lane >> 4;
+  const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
+  const int col0 = (bx * kNW + wave) * NTH * 16;    // first output column of this wave
+  const int n_rows = MODE == kGated && a.fused ? 2 * a.N : a.N;  // rows of one expert's matrix
+  const int nbr = (n_rows + kFp8Block - 1) / kFp8Block;
+
+  // this lane's row of each weight tile (clamped; what a tile past the end
+  // computes is not stored)
+  const uint8_t *wp[kNT];
+  int sidx[kNT];  // which of the NS scales
+  const int up0 = MODE == kGated && a.fused ? a.N : 0;
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+    const bool up = MODE == kGated && nt >= NTH;
+    const int col = min(col0 + (nt % NTH) * 16, a.N - 16);
+    const int row = col + (up ? up0 : 0);
+    const uint8_t *base = up && !a.fused ? a.w1 : a.w0;
+    wp[nt] = base + (int64_t(tile.expert) * n_rows + row + lr) * K + lg * 16;
+    if (MODE == kGated)
+      sidx[nt] = up ? 1 + (row / kFp8Block - (up0 + bx * COLS) / kFp8Block) : 0;
+    else
+      sidx[nt] = min(col / kFp8Block - bx * (COLS / kFp8Block), 1);
+    sidx[nt] = __builtin_amdgcn_readfirstlane(max(sidx[nt], 0));
+  }
+  // staging of the rows' codes: pass p of a thread -> row 32 p + tid / 8, piece tid % 8
+  const int piece = tid % kPieces;
+  const uint8_t *ap[PPT];
+  bool aok[PPT];
+#pragma unroll
+  for (int p = 0; p < PPT; ++p) {
+    const int m = p * (kThreads / kPieces) + tid / kPieces;
+    const int r = m < tile.rows ? source_row(a, tile.row0 + m) : -1;
+    aok[p] = r >= 0;
+    ap[p] = static_cast<const uint8_t *>(a.a) + int64_t(max(r, 0)) * K;
+  }
+  // staging of the scales: value q of a thread -> scale q / BM, row q % BM
+  const float *sap[SPT], *swp[SPT];
+  bool sok[SPT];
+#pragma unroll
+  for (int q = 0; q < SPT; ++q) {
+    const int v = min(tid + q * kThreads, BM * NS - 1), m = v % BM, s = v / BM;
+    const int r = m < tile.rows ? source_row(a, tile.row0 + m) : -1;
+    sok[q] = r >= 0;
+    sap[q] = a.as + max(r, 0);
+    int blk;
+    if (MODE == kGated) blk = s == 0 ? bx * COLS / kFp8Block : (up0 + bx * COLS) / kFp8Block + s - 1;
+    else blk = bx * (COLS / kFp8Block) + s;
+    const float *base = MODE == kGated && s > 0 && !a.fused ? a.s1 : a.s0;
+    swp[q] = base + (int64_t(tile.expert) * nbr + min(blk, nbr - 1)) * nb;
+  }
+
+  uint4 stg[PPT];
+  float sst[SPT];
+  uint4 wn[kNT][2];
+  auto load = [&](int s) {
+    s = min(s, nb - 1);
+    const int k0 = s * kFp8Block;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      wn[nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0, K - 16 - lg * 16));
+      wn[nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0 + 64, K - 16 - lg * 16));
+    }
+#pragma unroll
+    for (int p = 0; p < PPT; ++p) stg[p] = *reinterpret_cast<const uint4 *>(ap[p] + min(k0 + piece * 16, K - 16));
+#pragma unroll
+    for (int q = 0; q < SPT; ++q) sst[q] = sap[q][int64_t(s) * a.a_rows] * swp[q][s];
+  };
+  auto stage = [&](int s) {  // into buffer s % 2
+    const int buf = s & 1, k0 = s * kFp8Block;
+#pragma unroll
+    for (int p = 0; p < PPT; ++p) {
+      const int m = p * (kThreads / kPieces) + tid / kPieces;
+      *reinterpret_cast<uint4 *>(&sa[buf][m][piece * 16]) = keep(stg[p], aok[p] && k0 + piece * 16 < K);
+    }
+#pragma unroll
+    for (int q = 0; q < SPT; ++q) {
+      const int v = tid + q * kThreads;
+      if (v < BM * NS) ss[buf][v / BM][v % BM] = sok[q] ? sst[q] : 0.f;
+    }
+  };
+
+  fp8_acc acc[kNT][RB];
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) acc[nt][mt] = fp8_acc{0.f, 0.f, 0.f, 0.f};
+
+  load(0);
+  stage(0);
+  __syncthreads();
+  for (int s = 0; s < nb; ++s) {
+    const int buf = s & 1, k0 = s * kFp8Block;
+    // the codes past the end of the reduction are zero in both operands (a
+    // stray code may be a NaN, which a zero in the other operand keeps)
+    const bool ok0 = k0 + lg * 16 < K, ok1 = k0 + 64 + lg * 16 < K;
+    auto codes = [&](int nt) { return Fp8Operand<EXACT>(join8(keep(wn[nt][0], ok0), keep(wn[nt][1], ok1))); };
+    const Fp8Operand<EXACT> w[kNT] = {codes(0), codes(1), codes(2), codes(3)};
+    load(s + 1);
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) {
+      const uint8_t *row = &sa[buf][mt * 16 + lr][lg * 16];
+      const Fp8Operand<EXACT> x(
+          join8(*reinterpret_cast<const uint4 *>(row), *reinterpret_cast<const uint4 *>(row + 64)));
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const float sc = ss[buf][sidx[nt]][mt * 16 + lr];
+        const fp8_acc d = fp8_product(w[nt], x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][mt][i] = __builtin_fmaf(d[i], sc, acc[nt][mt][i]);
+      }
+    }
+    if (s + 1 < nb) stage(s + 1);
+    __syncthreads();
+  }
+
+  if constexpr (MODE == kPlain) {
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) {
+      const int m = mt * 16 + lr;
+      if (m < tile.rows) {
+        const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+          if (col0 + nt * 16 < a.N) store4(a, at + col0 + nt * 16, acc[nt][mt]);
+      }
+    }
+  } else {
+    // h = the gated unit, its maxima over the workgroup's 128 columns, codes
+    const bool ok[2] = {col0 < a.N, col0 + 16 < a.N};
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) {
+      float mx = 0.f;
+      with_glu(a.round, a.geglu, [&](auto rt, auto gt) {
+#pragma unroll
+        for (int nt = 0; nt < NTH; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float h = glu_t<decltype(rt)::value, decltype(gt)::value>(acc[nt][mt][i], acc[nt + NTH][mt][i]);
+            acc[nt][mt][i] = h;
+            if (ok[nt]) mx = fmaxf(mx, fabsf(h));
+          }
+      });
+      mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
+      mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
+      if (lg == 0) rmax[wave][mt * 16 + lr] = mx;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) {
+      const int m = mt * 16 + lr;
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < kNW; ++i) mx = fmaxf(mx, rmax[i][m]);
+      const Fp8Quant q(mx);
+      if (m < tile.rows) {
+        const int64_t row = tile.row0 + m;
+        uint8_t *h = static_cast<uint8_t *>(a.out) + row * a.N + col0 + 4 * lg;
+#pragma unroll
+        for (int nt = 0; nt < NTH; ++nt) {
+          const fp8_acc &v = acc[nt][mt];
+          if (ok[nt]) *reinterpret_cast<uint32_t *>(h + nt * 16) = fp8_pack4(q(v[0]), q(v[1]), q(v[2]), q(v[3]));
+        }
+        if (wave == 0 && lg == 0) a.hs[int64_t(bx) * a.rows + row] = q.scale;
+      }
+    }
+  }
+}
+
+template <int RB, int MODE, bool EXACT>
+__global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
+  tile_body<RB, MODE, EXACT>(a);
+}
+
+// The decode kernel: 16 token rows by WN weight tiles per wave; KW of the
+// four waves split the reduction, the others take further columns.  SRC:
+// codes, or the type of the values that it quantises.
+template <int KW, int WN, int MODE, int SRC>
+__global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
+  constexpr int NTH = MODE == kGated ? WN / 2 : WN;
+  constexpr int COLS = (kNW / KW) * NTH * 16;
+  constexpr int XB = SRC == kSrcCodes ? 1 : SRC == kDtF32 ? 4 : 2;  // bytes per activation
+  constexpr int DEPTH = WN >= 4 || XB == 4 ? 2 : 4;                  // blocks in flight per wave
+  __shared__ float part[KW > 1 ? kNW : 1][KW > 1 ? WN * 4 : 1][kWave];
+
+  const int nbx = (a.N + COLS - 1) / COLS;
+  PlanItem tile;
+  int bx;
+  if (!my_work(a, 16, nbx, tile, bx)) return;
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const int lr = lane & 15, lg = lane >> 4;
+  const int kz = wave % KW;
+  const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
+  const int per = (nb + KW - 1) / KW, sbeg = min(kz * per, nb), send = min(sbeg + per, nb);
+  const int col0 = (bx * (kNW / KW) + wave / KW) * NTH * 16;
+  const int n_rows = MODE == kGated && a.fused ? 2 * a.N : a.N;
+  const int nbr = (n_rows + kFp8Block - 1) / kFp8Block;
+
+  const uint8_t *wp[WN];
+  const float *sp[WN];  // scales of each tile's block row
+#pragma unroll
+  for (int nt = 0; nt < WN; ++nt) {
+    const bool up = MODE == kGated && nt >= NTH;
+    const int row = min(col0 + (nt % NTH) * 16, a.N - 16) + (up && a.fused ? a.N : 0);
+    const bool second = up && !a.fused;
+    wp[nt] = (second ? a.w1 : a.w0) + (int64_t(tile.expert) * n_rows + row + lr) * K + lg * 16;
+    sp[nt] = (second ? a.s1 : a.s0) + (int64_t(tile.expert) * nbr + row / kFp8Block) * nb;
+  }
+  const int r = lr < tile.rows ? source_row(a, tile.row0 + lr) : -1;
+  const bool rok = r >= 0;
+  const char *xp = static_cast<const char *>(a.a) + int64_t(max(r, 0)) * K * XB;
+  const float *sxp = SRC == kSrcCodes ? a.as + max(r, 0) : nullptr;
+
+  uint4 wq[DEPTH][WN][2], xq[DEPTH][2][XB];
+  float sq[DEPTH][WN], sx[DEPTH];
+  auto load = [&](int s, int d) {
+    const int k0 = s * kFp8Block;
+#pragma unroll
+    for (int nt = 0; nt < WN; ++nt) {
+      wq[d][nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0, K - 16 - lg * 16));
+      wq[d][nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0 + 64, K - 16 - lg * 16));
+      sq[d][nt] = sp[nt][s];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int u = 0; u < XB; ++u)
+        xq[d][h][u] = reinterpret_cast<const uint4 *>(xp + int64_t(min(k0 + 64 * h + lg * 16, K - 16)) * XB)[u];
+    if constexpr (SRC == kSrcCodes) sx[d] = sxp[int64_t(s) * a.a_rows];
+  };
+  fp8_acc acc[WN];
+#pragma unroll
+  for (int nt = 0; nt < WN; ++nt) acc[nt] = fp8_acc{0.f, 0.f, 0.f, 0.f};
+
+  auto use = [&](int s, int d) {
+    const int k0 = s * kFp8Block;
+    const bool ok[2] = {k0 + lg * 16 < K, k0 + 64 + lg * 16 < K};
+    i32x8 x;
+    if constexpr (SRC == kSrcCodes) {
+      x = join8(keep(xq[d][0][0], ok[0] && rok), keep(xq[d][1][0], ok[1] && rok));
+    } else {
+      float v[2][16], mx = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int u = 0; u < XB; ++u) {
+          const uint4 f = keep(xq[d][h][u], ok[h] && rok);
+          const uint32_t g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (SRC == kDtF32) v[h][4 * u + j] = __uint_as_float(g[j]);
+            else v[h][8 * u + 2 * j] = half_lo<SRC>(g[j]), v[h][8 * u + 2 * j + 1] = half_hi<SRC>(g[j]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[h][i]));
+      }
+      mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
+      mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
+      const Fp8Quant q(mx);
+      sx[d] = q.scale;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float *u = &v[j / 4][4 * (j % 4)];
+        x[j] = int(fp8_pack4(q(u[0]), q(u[1]), q(u[2]), q(u[3])));
+      }
+    }
+    const Fp8Operand<true> xo(x);
+    const float sxv = rok ? sx[d] : 0.f;
+#pragma unroll
+    for (int nt = 0; nt < WN; ++nt) {
+      const fp8_acc v =
+          fp8_product(Fp8Operand<true>(join8(keep(wq[d][nt][0], ok[0]), keep(wq[d][nt][1], ok[1]))), xo);
+      const float sc = sxv * sq[d][nt];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][i] = __builtin_fmaf(v[i], sc, acc[nt][i]);
+    }
+  };
+  // (a wave without blocks of its own loads the last one and uses none)
+  const int last = max(send - 1, sbeg < nb ? sbeg : nb - 1);
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) load(min(sbeg + d, last), d);
+  int s0 = sbeg;
+  for (; s0 + DEPTH < send; s0 += DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      use(s0 + d, d);
+      load(min(s0 + DEPTH + d, last), d);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (s0 + d < send) use(s0 + d, d);
+  if constexpr (KW > 1) {  // the parts of the reduction, added in their order
+    if (kz) {
+#pragma unroll
+      for (int nt = 0; nt < WN; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[wave][nt * 4 + i][lane] = acc[nt][i];
+    }
+    __syncthreads();
+    if (kz) return;
+#pragma unroll
+    for (int z = 1; z < KW; ++z)
+#pragma unroll
+      for (int nt = 0; nt < WN; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][i] += part[wave + z][nt * 4 + i][lane];
+  }
+  if (lr >= tile.rows) return;
+  const int64_t at = int64_t(tile.row0 + lr) * a.N + 4 * lg;
+#pragma unroll
+  for (int nt = 0; nt < NTH; ++nt) {
+    const int col = col0 + nt * 16;
+    if (col < a.N) {
+      fp8_acc v = acc[nt];
+      if constexpr (MODE == kGated) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = glu(acc[nt][i], acc[nt + NTH][i], a.round, a.geglu);
+      }
+      store4(a, at + col, v);
+    }
+  }
+}
+
+// Row tiles that the experts' rows can take at most: each expert adds at most
+// one partly filled tile.
+
+
+int64_t most_tiles(int64_t rows, int experts, int bm) {
+  return rows / bm + std::min<int64_t>(rows, experts);
+}
+
+template <int RB, int MODE, bool EXACT>
+void launch_tile(const Fp8Args &a, int64_t tiles, hipStream_t s) {
+  constexpr int COLS = MODE == kGated ? kBN / 2 : kBN;
+  const int64_t nbx = (a.N + COLS - 1) / COLS;
+  launch((fp8_tile_kernel<RB, MODE, EXACT>), dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
+}
+
+template <int KW, int WN, int MODE, int SRC>
+void launch_decode_one(const Fp8Args &a, int64_t tiles, hipStream_t s) {
+  constexpr int COLS = (kNW / KW) * (MODE == kGated ? WN / 2 : WN) * 16;
+  const int64_t nbx = (a.N + COLS - 1) / COLS;
+  launch((fp8_decode_kernel<KW, WN, MODE, SRC>), dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
+}
+
+// Waves that split the reduction of the decode kernel.
+int decode_split(int K) {
+  const int nb = (K + kFp8Block - 1) / kFp8Block;
+  return nb >= 8 ? 4 : nb >= 4 ? 2 : 1;
+}
+// Output columns per workgroup of the decode kernel.
+int decode_cols(int K, bool gated) { return kNW / decode_split(K) * (gated ? 1 : 2) * 16; }
+
+template <int MODE, int SRC>
+void launch_decode(const Fp8Args &a, int64_t tiles, hipStream_t s) {
+  const int kw = decode_split(a.K);
+  if (kw == 4) launch_decode_one<4, 2, MODE, SRC>(a, tiles, s);
+  else if (kw == 2) launch_decode_one<2, 2, MODE, SRC>(a, tiles, s);
+  else launch_decode_one<1, 2, MODE, SRC>(a, tiles, s);
+}
+
+}  // namespace
+
+int64_t fp8_matmul_groups(int64_t rows, int32_t N, int32_t K, int32_t n_experts, bool offsets, bool exact) {
+  const int bm = fp8_tile_rows(rows, n_experts, exact);
+  const int64_t tiles = offsets ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
+  const int cols = bm == 16 ? decode_cols(K, false) : kBN;
+  return tiles * ((N + cols - 1) / cols);
+}
+
+static int64_t ffn_tiles(const moe_layer_desc *d, int32_t T) {
+  const int bm = plan_tile_rows(d, T);
+  return most_tiles(int64_t(T) * d->top_k, d->n_experts, bm) + int64_t(d->n_shared) * ((T + bm - 1) / bm);
+}
+
+int64_t fp8_ffn_groups(const moe_layer_desc *d, int32_t T) {
+  const bool dec = plan_tile_rows(d, T) == 16;
+  const int gc = dec ? decode_cols(d->d_model, true) : kBN / 2, dc = dec ? decode_cols(d->d_ff, false) : kBN;
+  return ffn_tiles(d, T) * std::max((d->d_ff + gc - 1) / gc, (d->d_model + dc - 1) / dc);
+}
+
+// Rows per tile, by the mean rows of an expert: 16 (the decode kernel), 64,
+// or 128 where the 8-bit instruction is used.
+int fp8_tile_rows(int64_t rows, int experts, bool exact) {
+  return rows <= 16LL * experts ? 16 : exact || rows <= 96LL * experts ? 64 : 128;
+}
+
+void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_t a_rows, const uint8_t *a,
+                       const float *a_scales, const int32_t *row_map, const int32_t *expert_off, const uint8_t *w,
+                       const float *w_scales, void *y, int32_t out_dtype, void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Fp8Args g{};
+  g.a = a, g.as = a_scales, g.a_rows = a_rows, g.row_map = row_map;
+  g.rows = rows, g.N = N, g.K = K;
+  g.w0 = w, g.s0 = w_scales;
+  g.E = n_experts, g.expert_off = expert_off;
+  g.out = y, g.out_dtype = out_dtype;
+  const bool exact = out_dtype == MOE_DT_F32;
+  const int bm = fp8_tile_rows(rows, n_experts, exact);
+  const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
+  if (bm == 16) launch_decode<kPlain, kSrcCodes>(g, tiles, s);
+  else if (exact) launch_tile<4, kPlain, true>(g, tiles, s);
+  else if (bm == 64) launch_tile<4, kPlain, false>(g, tiles, s);
+  else launch_tile<8, kPlain, false>(g, tiles, s);
+}
+
+// Workspace of the expert FFN: x codes and scales (tile kernels), h as codes
+// and scales or as fp32.
+void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, const int32_t *row_map,
+                           const moe_weights *w, const int32_t *counters, const PlanItem *tiles,
+                           const FfnScratch &sc, float *y_sorted, void *stream, StageMarker *mk) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t max_tiles = ffn_tiles(d, T);
+  const int D = d->d_model, F = d->d_ff, M = d->n_experts + d->n_shared;
+  const int N = T * d->top_k, R = N + d->n_shared * T;
+  const moe_proj &pg = d->gate_up_fused ? w->gate_up : w->gate;
+  const int bm = plan_tile_rows(d, T);
+  Fp8Args g{};
+  g.row_map = row_map, g.rows = R, g.N = F, g.K = D, g.T = T, g.n_routed = N;
+  g.w0 = static_cast<const uint8_t *>(pg.w), g.s0 = static_cast<const float *>(pg.scales);
+  g.w1 = static_cast<const uint8_t *>(w->up.w), g.s1 = static_cast<const float *>(w->up.scales);
+  g.fused = d->gate_up_fused, g.round = glu_round_mode(d), g.geglu = d->activation == MOE_ACT_GEGLU;
+  g.E = M, g.tiles = tiles, g.counters = counters;
+  g.a_rows = T;
+  g.out = sc.h;
+  Fp8Args n{};
+  n.rows = R, n.N = D, n.K = F;
+  n.w0 = static_cast<const uint8_t *>(w->down.w), n.s0 = static_cast<const float *>(w->down.scales);
+  n.E = M, n.tiles = tiles, n.counters = counters;
+  n.a = sc.h, n.a_rows = R;
+  n.out = y_sorted, n.out_dtype = MOE_DT_F32;
+  if (bm == 16) {  // both projections quantise their own rows; h is fp32
+    g.a = x;
+    g.out_dtype = MOE_DT_F32;
+    if (d->act_dtype == MOE_DT_BF16) launch_decode<kGated, kDtBF16>(g, max_tiles, s);
+    else if (d->act_dtype == MOE_DT_F16) launch_decode<kGated, kDtF16>(g, max_tiles, s);
+    else launch_decode<kGated, kDtF32>(g, max_tiles, s);
+    if (mk) mk->mark("gateup_fp8");
+    launch_decode<kPlain, kDtF32>(n, max_tiles, s);
+    if (mk) mk->mark("down_fp8");
+    return;
+  }
+  uint8_t *xq = static_cast<uint8_t *>(sc.x16);
+  float *xs = reinterpret_cast<float *>(sc.xg);
+  float *hs = reinterpret_cast<float *>(sc.hsh);
+  launch_fp8_rows(x, d->act_dtype, T, D, xq, xs, stream);
+  if (mk) mk->mark("x_fp8");
+  g.a = xq, g.as = xs, g.hs = hs;
+  n.as = hs;
+  launch_tile<4, kGated, true>(g, max_tiles, s);
+  if (mk) mk->mark("gateup_fp8");
+  launch_tile<4, kPlain, true>(n, max_tiles, s);
+  if (mk) mk->mark("down_fp8");
+}
+
+}  // namespace moe

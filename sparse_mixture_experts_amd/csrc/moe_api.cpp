@@ -25,6 +25,8 @@ int hip_status() {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
+bool valid_dtype(int32_t t) { return t == MOE_DT_F32 || t == MOE_DT_BF16 || t == MOE_DT_F16; }
+
 template <class T>
 T *at(void *ws, size_t off) {
   return reinterpret_cast<T *>(static_cast<char *>(ws) + off);
@@ -37,6 +39,7 @@ FfnScratch ffn_scratch(void *ws, const Workspace &L, bool x16_ready) {
 
 int check_ws(const moe_layer_desc *d, int32_t T, const void *ws, size_t ws_bytes, Workspace *out) {
   *out = workspace_layout(d, T);
+  if (fp8(d) && fp8_ffn_groups(d, T) > kMaxGroups) return MOE_E_INVALID;
   if (validate_ptr(ws)) return MOE_E_INVALID;
   if (ws_bytes < out->total) return MOE_E_WORKSPACE;
   return MOE_OK;
@@ -270,6 +273,52 @@ int moe_pack_weights(const moe_layer_desc *desc, int32_t proj, const void *w, co
     return s;
   launch_pack(desc, proj, static_cast<const uint32_t *>(w), static_cast<const uint16_t *>(scales),
               static_cast<const uint16_t *>(biases), w_packed, stream);
+  return hip_status();
+}
+
+int moe_fp8_quantize(int32_t n_matrices, int32_t rows, int32_t cols, const void *x, int32_t dtype, int32_t block_rows,
+                     uint8_t *codes, float *scales, void *stream) {
+  int s;
+  if (n_matrices < 0 || rows < 0 || cols <= 0 || cols % 16) return MOE_E_INVALID;
+  if (!valid_dtype(dtype) || (block_rows != 1 && block_rows != 128)) return MOE_E_INVALID;
+  if ((s = validate_ptr(x)) || (s = validate_ptr(codes)) || (s = validate_ptr(scales))) return s;
+  const int64_t all = int64_t(n_matrices) * rows, nbc = (cols + 127) / 128;
+  if (all == 0) return MOE_OK;
+  const int64_t groups = block_rows == 1 ? (all + 31) / 32 * nbc : int64_t(n_matrices) * ((rows + 127) / 128) * nbc;
+  if (all > INT32_MAX || groups > kMaxGroups) return MOE_E_INVALID;
+  if (block_rows == 1) launch_fp8_rows(x, dtype, int32_t(all), cols, codes, scales, stream);
+  else launch_fp8_blocks(x, dtype, n_matrices, rows, cols, codes, scales, stream);
+  return hip_status();
+}
+
+int moe_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_t a_rows, const uint8_t *a,
+                   const float *a_scales, const int32_t *row_map, const int32_t *expert_off, const uint8_t *w,
+                   const float *w_scales, void *y, int32_t out_dtype, void *stream) {
+  int s;
+  if (rows < 0 || a_rows < 0 || N <= 0 || K <= 0 || N % 16 || K % 16 || int64_t(N) * K > (int64_t(1) << 31))
+    return MOE_E_INVALID;
+  if (n_experts < 1 || n_experts > kMaxExperts || !valid_dtype(out_dtype)) return MOE_E_INVALID;
+  if ((s = validate_ptr(a)) || (s = validate_ptr(a_scales)) || (s = validate_ptr(row_map, true)) ||
+      (s = validate_ptr(expert_off, n_experts == 1)) || (s = validate_ptr(w)) || (s = validate_ptr(w_scales)) ||
+      (s = validate_ptr(y)))
+    return s;
+  if (rows == 0) return MOE_OK;
+  if (a_rows < (row_map ? 1 : rows)) return MOE_E_INVALID;
+  if (fp8_matmul_groups(rows, N, K, n_experts, expert_off != nullptr, out_dtype == MOE_DT_F32) > kMaxGroups) return MOE_E_INVALID;
+  launch_fp8_matmul(rows, N, K, n_experts, a_rows, a, a_scales, row_map, expert_off, w, w_scales, y, out_dtype,
+                    stream);
+  return hip_status();
+}
+
+int moe_fp8_transpose(int32_t n_matrices, int32_t N, int32_t K, const uint8_t *w, const float *w_scales, uint8_t *wt,
+                      float *wt_scales, void *stream) {
+  int s;
+  if (n_matrices < 0 || N <= 0 || K <= 0 || N % 16 || K % 16) return MOE_E_INVALID;
+  if ((s = validate_ptr(w)) || (s = validate_ptr(w_scales)) || (s = validate_ptr(wt)) || (s = validate_ptr(wt_scales)))
+    return s;
+  if (int64_t(n_matrices) * ((N + 127) / 128) * ((K + 127) / 128) > kMaxGroups) return MOE_E_INVALID;
+  if (n_matrices == 0) return MOE_OK;
+  launch_fp8_transpose(n_matrices, N, K, w, w_scales, wt, wt_scales, stream);
   return hip_status();
 }
 

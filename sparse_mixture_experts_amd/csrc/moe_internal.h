@@ -108,8 +108,13 @@ inline int64_t act_bytes(const moe_layer_desc *d) { return d->act_dtype == MOE_D
 inline bool affine(const moe_layer_desc *d) {
   return d->w_format == MOE_WF_AFFINE_Q4 || d->w_format == MOE_WF_AFFINE_Q8;
 }
-// Bytes per element of the GLU intermediate h (16-bit for bf16 and fp16 layers).
-inline int64_t h_bytes(const moe_layer_desc *d) { return d->act_dtype == MOE_DT_F32 ? 4 : 2; }
+// Bytes per element of the GLU intermediate h (16-bit for bf16 and fp16
+// layers; fp32, or codes in the same place, for fp8 layers).
+inline int64_t h_bytes(const moe_layer_desc *d) {
+  return d->act_dtype == MOE_DT_F32 || d->w_format == MOE_WF_FP8 ? 4 : 2;
+}
+// 8-bit floating point expert weights.
+inline bool fp8(const moe_layer_desc *d) { return d->w_format == MOE_WF_FP8; }
 bool use_mfma(const moe_layer_desc *d);
 // Per-op GLU rounding mode of the layer: 0 none, 1 bf16, 2 fp16 (the layer's
 // activation dtype).
@@ -128,9 +133,9 @@ struct Workspace {
   size_t act_items;                   // [E+S] PlanItem
   size_t tiles;                       // [max_tiles] PlanItem
   size_t h;                           // [N+S*T][d_ff] h_bytes (one token: [k+S][d_ff] fp32)
-  size_t hsh;                         // [N+S*T][ceil(d_ff/128)] int8 (affine layers)
-  size_t x16, xsh;                    // [T][d_model] fp16, [T] int8 (affine layers)
-  size_t xg;                          // [T][GP] fp16 group means of x16 (affine matrix-core layers)
+  size_t hsh;                         // [N+S*T][ceil(d_ff/128)] int8 (affine); h scales, fp32 (fp8)
+  size_t x16, xsh;                    // [T][d_model] fp16, [T] int8 (affine); x codes (fp8)
+  size_t xg;                          // [T][GP] fp16 group means of x16 (affine matrix cores); x scales, fp32 (fp8)
   size_t y_sorted;                    // [N+S*T][d_model]: fp16 (ys_f16e), fp32, or [parts] fp32 partial rows
   size_t ys_sh;                       // [N+S*T][d_model/64] int8 exponents (ys_f16e)
   size_t total;
@@ -303,6 +308,32 @@ void launch_backward_mfma(const moe_layer_desc *d, int32_t T, const void *x, con
 void launch_gate_up_raw_mfma(const moe_layer_desc *d, int32_t T, const void *x, const int32_t *row_map,
                              const moe_weights *w, const int32_t *counters, const PlanItem *tiles, int64_t max_tiles,
                              const FfnScratch &sc, float *gu, void *stream);
+
+// ---- 8-bit (e4m3) products --------------------------------------------------
+// Codes and scales of rows (one scale per 128 columns of a row, [block][row])
+// and of matrices (one per 128 x 128 block).
+void launch_fp8_rows(const void *x, int32_t dtype, int32_t rows, int32_t cols, uint8_t *codes, float *scales,
+                     void *stream);
+void launch_fp8_blocks(const void *x, int32_t dtype, int32_t matrices, int32_t rows, int32_t cols, uint8_t *codes,
+                       float *scales, void *stream);
+// Rows per tile of the grouped products (16, 64 or 128).  exact: fp32 sums of
+// 16-bit products (fp32 results and the layer), else the 8-bit instruction.
+int fp8_tile_rows(int64_t rows, int experts, bool exact);
+// Workgroups of the grids that the grouped product and the fp8 layer launch
+// (at most kMaxGroups: the threads of a grid are counted in 32 bits).
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
+int64_t fp8_matmul_groups(int64_t rows, int32_t N, int32_t K, int32_t n_experts, bool offsets,
+                          bool exact);
+int64_t fp8_ffn_groups(const moe_layer_desc *d, int32_t T);
+void launch_fp8_transpose(int32_t n_matrices, int32_t N, int32_t K, const uint8_t *w, const float *w_scales,
+                          uint8_t *wt, float *wt_scales, void *stream);
+void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_t a_rows, const uint8_t *a,
+                       const float *a_scales, const int32_t *row_map, const int32_t *expert_off, const uint8_t *w,
+                       const float *w_scales, void *y, int32_t out_dtype, void *stream);
+// The expert FFN of an fp8 layer over the plan, y_sorted fp32.
+void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, const int32_t *row_map,
+                           const moe_weights *w, const int32_t *counters, const PlanItem *tiles,
+                           const FfnScratch &sc, float *y_sorted, void *stream, StageMarker *mk);
 
 // Combine.
 // Combine of fp32 rows (ys_sh null), fp16 rows with exponents ys_sh, or

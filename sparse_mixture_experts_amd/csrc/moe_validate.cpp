@@ -13,7 +13,7 @@ int validate_desc(const moe_layer_desc *d) {
   if (!d) return MOE_E_INVALID;
   if (d->act_dtype != MOE_DT_F32 && d->act_dtype != MOE_DT_BF16 && d->act_dtype != MOE_DT_F16)
     return MOE_E_INVALID;
-  if (d->w_format != MOE_WF_DENSE && !affine(d)) return MOE_E_INVALID;
+  if (d->w_format != MOE_WF_DENSE && !affine(d) && !fp8(d)) return MOE_E_INVALID;
   if (!is_bool(d->gate_up_fused) || !is_bool(d->glu_round) || !is_bool(d->renormalize))
     return MOE_E_INVALID;
   if (d->activation != MOE_ACT_SWIGLU && d->activation != MOE_ACT_GEGLU) return MOE_E_INVALID;
@@ -30,6 +30,8 @@ int validate_desc(const moe_layer_desc *d) {
     const int g = d->group_size;
     if (g != 32 && g != 64 && g != 128) return MOE_E_UNSUPPORTED;
     if (d->d_model % 64 || d->d_ff % 64 || d->d_model % g || d->d_ff % g) return MOE_E_INVALID;
+  } else if (fp8(d)) {
+    if (d->d_model % 16 || d->d_ff % 16) return MOE_E_INVALID;
   } else {
     if (d->d_model % 8 || d->d_ff % 8) return MOE_E_INVALID;
   }
@@ -55,6 +57,9 @@ static int validate_proj(const moe_layer_desc *d, const moe_proj &p) {
     if ((s = validate_ptr(p.scales))) return s;
     if ((s = validate_ptr(p.biases))) return s;
     if ((s = validate_ptr(p.w_packed, true))) return s;
+  } else if (fp8(d)) {
+    if ((s = validate_ptr(p.scales))) return s;
+    if (p.biases || p.w_packed) return MOE_E_INVALID;
   } else if (p.w_packed) {
     return MOE_E_INVALID;  // the packed copy exists for affine codes only
   }
@@ -171,11 +176,12 @@ Workspace workspace_layout(const moe_layer_desc *d, int32_t T) {
   // 16-bit rows of two tokens already cover, so the size stays non-decreasing in T
   const int64_t h_one_token = T >= 1 ? (int64_t(d->top_k) + S) * d->d_ff * 4 : 0;
   ws.h = take(size_t(std::max<int64_t>(rows * d->d_ff * h_bytes(d), h_one_token)));
-  const bool q4 = affine(d);
-  ws.hsh = take(q4 ? size_t(rows) * ((d->d_ff + kHBlock - 1) / kHBlock) : 0);
-  ws.x16 = take(q4 ? size_t(T) * d->d_model * 2 : 0);
+  const bool q4 = affine(d), f8 = fp8(d);
+  const size_t hblk = (d->d_ff + kHBlock - 1) / kHBlock, xblk = (d->d_model + kHBlock - 1) / kHBlock;
+  ws.hsh = take(q4 ? size_t(rows) * hblk : f8 ? size_t(rows) * hblk * 4 : 0);
+  ws.x16 = take(q4 ? size_t(T) * d->d_model * 2 : f8 ? size_t(T) * d->d_model : 0);
   ws.xsh = take(q4 ? size_t(T) : 0);
-  ws.xg = take(q4 && use_mfma(d) ? size_t(T) * xg_groups_padded(d) * 2 : 0);
+  ws.xg = take(q4 && use_mfma(d) ? size_t(T) * xg_groups_padded(d) * 2 : f8 ? size_t(T) * xblk * 4 : 0);
   ws.y_sorted = take(size_t(ys_workspace_bytes(d, T)));
   ws.ys_sh = take(use_mfma(d) ? size_t(rows) * (d->d_model / kYsBlock) : 0);
   ws.total = o;

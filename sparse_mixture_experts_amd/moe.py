@@ -20,14 +20,15 @@ LIB_PATH = os.path.join(_PKG, "libmoe_mi355x.so")
 MOE_OK, MOE_E_INVALID, MOE_E_UNSUPPORTED, MOE_E_WORKSPACE, MOE_E_HIP = 0, -1, -2, -3, -4
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 0, 1, 2
 _DT = {"f32": MOE_DT_F32, "bf16": MOE_DT_BF16, "f16": MOE_DT_F16}
-MOE_WF_DENSE, MOE_WF_AFFINE_Q4, MOE_WF_AFFINE_Q8 = 0, 1, 2
+MOE_WF_DENSE, MOE_WF_AFFINE_Q4, MOE_WF_AFFINE_Q8, MOE_WF_FP8 = 0, 1, 2, 4
 MOE_ACT_SWIGLU, MOE_ACT_GEGLU = 0, 1
-_WFMT = {"dense": MOE_WF_DENSE, "q4": MOE_WF_AFFINE_Q4, "q8": MOE_WF_AFFINE_Q8}
+_WFMT = {"dense": MOE_WF_DENSE, "q4": MOE_WF_AFFINE_Q4, "q8": MOE_WF_AFFINE_Q8, "fp8": MOE_WF_FP8}
 _ACT = {"swiglu": MOE_ACT_SWIGLU, "geglu": MOE_ACT_GEGLU}
 
 EXPORTED = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
             "moe_forward", "moe_forward_timed", "moe_backward_workspace_size", "moe_backward",
-            "moe_status_string", "moe_forward_noalloc", "moe_packed_bytes", "moe_pack_weights")
+            "moe_status_string", "moe_forward_noalloc", "moe_packed_bytes", "moe_pack_weights",
+            "moe_fp8_quantize", "moe_fp8_matmul", "moe_fp8_transpose")
 MOE_PROJ_GATE, MOE_PROJ_UP, MOE_PROJ_GATE_UP, MOE_PROJ_DOWN = 0, 1, 2, 3
 _PROJ = {"gate": MOE_PROJ_GATE, "up": MOE_PROJ_UP, "gate_up": MOE_PROJ_GATE_UP, "down": MOE_PROJ_DOWN}
 NOALLOC_SCRATCH_BYTES = 96 * 1024 * 1024  # MOE_NOALLOC_SCRATCH_BYTES
@@ -83,6 +84,9 @@ def load() -> ctypes.CDLL:
         lib.moe_stream_read.argtypes = [vp, sz, vp, i32, vp]
         lib.moe_router_packed_bytes.argtypes = [P(LayerDesc), P(sz)]
         lib.moe_pack_router.argtypes = [P(LayerDesc), vp, vp, vp]
+        lib.moe_fp8_quantize.argtypes = [i32, i32, i32, vp, i32, i32, vp, vp, vp]
+        lib.moe_fp8_matmul.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp]
+        lib.moe_fp8_transpose.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp]
         lib.moe_status_string.argtypes = [ctypes.c_int]
         lib.moe_status_string.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -99,8 +103,8 @@ def moe_status_string(status: int) -> str:
 def make_desc(d_model, d_ff, n_experts, top_k, n_shared=0, act="bf16", wfmt="dense", group_size=64,
               gate_up_fused=False, glu_round=False, renormalize=True,
               activation="swiglu") -> LayerDesc:
-    """act: "f32", "bf16" or "f16"; wfmt: "dense", "q4" or "q8" (affine 4-/8-bit codes); activation:
-    "swiglu" or "geglu"."""
+    """act: "f32", "bf16" or "f16"; wfmt: "dense", "q4" or "q8" (affine 4-/8-bit codes) or
+    "fp8" (e4m3 codes); activation: "swiglu" or "geglu"."""
     return LayerDesc(d_model, d_ff, n_experts, top_k, n_shared,
                      _DT[act],
                      _WFMT[wfmt], group_size,
@@ -232,6 +236,28 @@ def moe_pack_weights(desc, proj: int, w, scales, biases, w_packed, stream=None):
     `biases`) into `w_packed` (moe_packed_bytes bytes)."""
     _check(load().moe_pack_weights(ctypes.byref(desc), proj, _ptr(w), _ptr(scales), _ptr(biases), _ptr(w_packed),
                                    _stream(stream)), "moe_pack_weights")
+
+
+def moe_fp8_quantize(n_matrices, rows, cols, x, dtype, block_rows, codes, scales, stream=None):
+    """e4m3 codes and fp32 scales of x [n_matrices][rows][cols]: one scale per 128 columns of a row
+    (block_rows 1, scales [blocks][n_matrices * rows]) or per 128 x 128 block (block_rows 128)."""
+    _check(load().moe_fp8_quantize(n_matrices, rows, cols, _ptr(x), dtype, block_rows, _ptr(codes), _ptr(scales),
+                                   _stream(stream)), "moe_fp8_quantize")
+
+
+def moe_fp8_matmul(rows, N, K, n_experts, a_rows, a, a_scales, row_map, expert_off, w, w_scales, y, out_dtype,
+                   stream=None):
+    """y [rows][N] = the rows of codes a times the matrix of their expert; row_map and expert_off as
+    moe_dispatch writes them, or None (row p; one expert)."""
+    _check(load().moe_fp8_matmul(rows, N, K, n_experts, a_rows, _ptr(a), _ptr(a_scales), _ptr(row_map),
+                                 _ptr(expert_off), _ptr(w), _ptr(w_scales), _ptr(y), out_dtype, _stream(stream)),
+           "moe_fp8_matmul")
+
+
+def moe_fp8_transpose(n_matrices, N, K, w, w_scales, wt, wt_scales, stream=None):
+    """The transposed copy of weight codes [n_matrices][N][K] and of their block scales."""
+    _check(load().moe_fp8_transpose(n_matrices, N, K, _ptr(w), _ptr(w_scales), _ptr(wt), _ptr(wt_scales),
+                                    _stream(stream)), "moe_fp8_transpose")
 
 
 # ---- marshalling helpers ----------------------------------------------------
