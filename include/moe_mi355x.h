@@ -366,6 +366,52 @@ int moe_forward_noalloc(const moe_layer_desc *desc, int32_t T, const void *x,
 int moe_stream_read(const void *src, size_t bytes, uint32_t *out, int32_t blocks, void *stream);
 
 /*
+ * Balance loss of the router, per-expert counts, and the router's gradients.
+ * Logits l = x . w_router + router_bias (fp32 sums; not the fixed order of
+ * moe_route), p = softmax(l) over all experts.  The T tokens form n_seqs
+ * sequences (1..4096): sequence b is the tokens t with
+ * seq_off[b] <= t < seq_off[b+1] (int32 [n_seqs + 1], nondecreasing; NULL:
+ * one sequence of all T).  A token counts when it lies in a sequence and its
+ * token_mask byte is not 0 (NULL: all count); what other tokens' x holds
+ * (NaNs too) reaches no other row and no sum.  Per sequence b:
+ *   seq_tokens[b] = n_b, its counted tokens,
+ *   expert_counts[b][e] = c_be, their topk_idx entries equal to e,
+ *   prob_mean[b][e] = P_be, the mean of their p[.][e] (0 when n_b = 0),
+ *   loss = 1/B' sum_{n_b > 0} E / (k n_b) sum_e c_be P_be,
+ * B' the sequences with n_b > 0 (loss 0 when there is none); balanced experts
+ * give 1.  topk_idx [T][k] as moe_route writes it; entries outside [0, E) are
+ * not counted.  logits [T][E] fp32 receives l of every token, for the
+ * backward pass.  All outputs are overwritten; with T == 0 (arrays over
+ * tokens may then be NULL) the counts, means, loss and gradients are zeros.  w_format and the expert fields of desc play no
+ * part.
+ *
+ * moe_balance_loss_backward: with the counts and the routing held, the
+ * gradient of
+ *   dloss[0] * loss + sum_{t counted, j} dtopk_w[t][j] * topk_w[t][j]
+ * where topk_w are the routing weights of moe_route as functions of the
+ * logits (the softmax over the k selected experts when desc->renormalize is
+ * set, else p at each): dx [T][d_model] (zero rows for tokens that do not
+ * count), dw_router [d_model][n_experts], drouter_bias [n_experts], all
+ * fp32 and overwritten, each skipped when NULL (not all three).  dloss NULL
+ * is 1; dtopk_w NULL is 0.  logits, expert_counts and seq_tokens as the
+ * forward pass left them.  With dtopk_w = the gradient of a loss with respect
+ * to moe_forward's topk_w_out, this is the whole gradient of the router.
+ *
+ * ws: moe_balance_workspace_size bytes for this T and n_seqs, 16-byte
+ * aligned, for either call; nothing in it is kept between them.
+ */
+int moe_balance_workspace_size(const moe_layer_desc *desc, int32_t T, int32_t n_seqs, size_t *bytes);
+int moe_balance_loss(const moe_layer_desc *desc, int32_t T, const void *x, const void *w_router,
+                     const float *router_bias, const int32_t *topk_idx, const uint8_t *token_mask, int32_t n_seqs,
+                     const int32_t *seq_off, float *logits, int32_t *expert_counts, int32_t *seq_tokens,
+                     float *prob_mean, float *loss, void *ws, size_t ws_bytes, void *stream);
+int moe_balance_loss_backward(const moe_layer_desc *desc, int32_t T, const void *x, const void *w_router,
+                              const int32_t *topk_idx, const uint8_t *token_mask, int32_t n_seqs,
+                              const int32_t *seq_off, const float *logits, const int32_t *expert_counts,
+                              const int32_t *seq_tokens, const float *dloss, const float *dtopk_w, float *dx,
+                              float *dw_router, float *drouter_bias, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * ---- 8-bit floating point ---------------------------------------------------
  *
  * Codes are OCP e4m3 (4 significant bits, largest value 448, no infinities).

@@ -1,0 +1,749 @@
+// balance.hip -- the router's balance loss, per-expert counts, and their
+// gradients (with those of the routing weights) for x, the router and its
+// bias.
+//
+// With logits l[t][e] = x[t] . W[:, e] + bias[e], p = softmax(l), and for
+// sequence b its n_b counted tokens, c_be slots at expert e and mean
+// probability P_be:
+//   L = 1/B' sum_b E / (k n_b) sum_e c_be P_be,   B' sequences with n_b > 0.
+// Its gradient with the counts held fixed is, for a token of sequence b,
+//   dl = p (g - sum_e p_e g_e),  g_e = dL E c_be / (k n_b^2 B'),
+// which does not change when a constant is taken from all g_e: c_be enters as
+// its difference from the mean count, an exact integer, so that nearly
+// balanced experts keep the digits of their differences.  The routing
+// weights' gradient adds to dl through the softmax over the selected experts
+// (renormalised weights), or to g (plain ones).  Then
+//   dx = dl W^T,  dW = x^T dl,  dbias = sum_t dl.
+//
+// The three matrix products run on the 16-bit matrix cores with fp32 sums.
+// 16-bit operands enter the logits as they are.  Elsewhere fp32 values are
+// cut into three bf16 pieces of 8 significant bits each (24 in all, so
+// nothing is lost), fp16 values into two, and the products of pieces above
+// 2^-24 of the largest are added: 3 products for bf16 layers, 5 for fp16 and
+// 6 for fp32, each at 16 times the fp32 matrix rate.
+//
+// Softmax, sums over tokens and the loss are per-wave rows and two-level sums
+// in a fixed order: no floating-point atomics.
+#include <algorithm>
+
+#include "dequant_f16.h"
+#include "device_common.h"
+#include "launch.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;             // output rows and columns per workgroup
+constexpr int kStep = 64;             // reduction elements per LDS stage
+constexpr int kLds = kStep + 8;       // 16-bit elements per LDS row: 16 rows' 16-byte pieces on different banks
+constexpr int kChunkTokens = 4;       // tokens per wave of the row kernels
+
+// ---- the split products -----------------------------------------------------
+
+// One operand: element (row, k) at p[row * ld + k] (KC) or p[k * ld + row].
+struct Operand {
+  const void *p;
+  int64_t ld;
+  int rows;
+  int vec;  // rows start 16-byte aligned: whole pieces load as vectors
+};
+// Tokens that take part (the reduction of dW runs over tokens): null mask and
+// off for all of them.
+struct Tokens {
+  const uint8_t *mask;
+  const int32_t *off;  // [n + 1]
+  int n, T;
+};
+__device__ __forceinline__ void token_range(const Tokens &k, int &lo, int &hi) {
+  lo = 0, hi = k.T;
+  if (k.off) {
+    lo = min(max(k.off[0], 0), k.T);
+    hi = min(max(k.off[k.n], lo), k.T);
+  }
+}
+
+struct GemmArgs {
+  Operand a, b;
+  int K, per;          // reduction length, steps per part
+  float *out;          // [parts][a.rows][b.rows]
+  int64_t part;        // elements per part
+  const float *bias;   // nullable, added per column
+  Tokens tokens;       // MASK: reduction elements that take part
+};
+
+template <int DT>
+constexpr int pieces(bool native) {
+  return DT == kDtBF16 || native ? 1 : DT == kDtF16 ? 2 : 3;
+}
+
+// v as bf16 pieces: cut (not rounded) to 8 significant bits, the rest cut
+// again; the last piece is rounded.  A value without a finite rest keeps its
+// first piece alone.
+template <int P>
+__device__ __forceinline__ void split(float v, uint32_t (&out)[P]) {
+  if constexpr (P == 1) {
+    out[0] = f32_to_bf16_bits(v);
+  } else {
+    const uint32_t b = __float_as_uint(v);
+    out[0] = b >> 16;
+    float r = v - __uint_as_float(b & 0xffff0000u);
+    if (!(fabsf(v) < INFINITY)) r = 0.f, out[0] = f32_to_bf16_bits(v);
+    if constexpr (P == 2) {
+      out[1] = f32_to_bf16_bits(r);
+    } else {
+      const uint32_t c = __float_as_uint(r);
+      out[1] = c >> 16;
+      out[2] = f32_to_bf16_bits(r - __uint_as_float(c & 0xffff0000u));
+    }
+  }
+}
+
+// Staging of a 64 x 64 tile of one operand.  KC: a thread takes 16
+// consecutive reduction elements of one row; else 4 x 4 elements, turned
+// around in registers, so that LDS always holds [row][k].
+template <int DT, bool KC, bool NATIVE>
+struct Stage {
+  static constexpr int P = pieces<DT>(NATIVE);
+  float v[16];
+  static __device__ __forceinline__ float elt(const Operand &o, int64_t i) { return load_act<DT>(o.p, i); }
+  // n elements from i (vector loads where aligned and whole), zero past `have`.
+  template <int N>
+  static __device__ __forceinline__ void run(const Operand &o, int64_t i, int have, float *dst) {
+    if (o.vec && have >= N) {
+      if constexpr (DT == kDtF32) {
+#pragma unroll
+        for (int u = 0; u < N / 4; ++u) {
+          const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(o.p) + i + 4 * u);
+          dst[4 * u] = f.x, dst[4 * u + 1] = f.y, dst[4 * u + 2] = f.z, dst[4 * u + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < N / 4; ++u) {
+          const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(o.p) + i + 4 * u);
+          dst[4 * u] = half_lo<DT>(w.x), dst[4 * u + 1] = half_hi<DT>(w.x);
+          dst[4 * u + 2] = half_lo<DT>(w.y), dst[4 * u + 3] = half_hi<DT>(w.y);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u) dst[u] = u < have ? elt(o, i + u) : 0.f;
+    }
+  }
+  template <bool MASK>
+  __device__ __forceinline__ void load(const Operand &o, int row0, int k0, int K, const Tokens &tk, int lo, int hi) {
+    const int tid = threadIdx.x;
+    if constexpr (KC) {
+      const int r = row0 + tid / 4, k = k0 + tid % 4 * 16;
+      run<16>(o, int64_t(min(r, o.rows - 1)) * o.ld + k, r < o.rows ? K - k : 0, v);
+    } else {
+      const int k = k0 + tid / 16 * 4, r = row0 + tid % 16 * 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bool ok = k + j < K;
+        if constexpr (MASK) ok = ok && k + j >= lo && k + j < hi && (!tk.mask || tk.mask[k + j]);
+        run<4>(o, int64_t(ok ? k + j : 0) * o.ld + r, ok ? o.rows - r : 0, &v[4 * j]);
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t bits(float f, uint32_t (&q)[P]) {
+    if constexpr (NATIVE) q[0] = f32_to_f16_bits(f);
+    else split<P>(f, q);
+    return q[0];
+  }
+  __device__ __forceinline__ void store(uint16_t (&lds)[P][kTile][kLds]) {
+    const int tid = threadIdx.x;
+    if constexpr (KC) {
+      uint32_t w[P][8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        uint32_t x[P], y[P];
+        bits(v[2 * u], x), bits(v[2 * u + 1], y);
+#pragma unroll
+        for (int p = 0; p < P; ++p) w[p][u] = x[p] | (y[p] << 16);
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        uint4 *q = reinterpret_cast<uint4 *>(&lds[p][tid / 4][tid % 4 * 16]);
+        q[0] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+        q[1] = make_uint4(w[p][4], w[p][5], w[p][6], w[p][7]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // row i of the 4 x 4 elements
+        uint32_t x[4][P];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bits(v[4 * j + i], x[j]);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<uint2 *>(&lds[p][tid % 16 * 4 + i][tid / 16 * 4]) =
+              make_uint2(x[0][p] | (x[1][p] << 16), x[2][p] | (x[3][p] << 16));
+      }
+    }
+  }
+};
+
+// C[m][n] = sum_k A(m, k) B(n, k) over one part of the reduction.  A wave
+// makes 32 x 32 outputs (operand a of the matrix cores: columns n, so that a
+// lane's four results are neighbours in a row of C).  NATIVE: fp16 operands
+// multiplied as they are.  MASK: reduction elements outside `tokens` count as
+// zeros, whatever they hold.
+template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK>
+__global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
+  using SA = Stage<DTA, KCA, NATIVE>;
+  using SB = Stage<DTB, KCB, NATIVE>;
+  constexpr int PA = SA::P, PB = SB::P;
+  __shared__ __align__(16) uint16_t la[PA][kTile][kLds], lb[PB][kTile][kLds];
+  const int lane = lane_id(), wave = threadIdx.x / kWave, lr = lane & 15, lg = lane >> 4;
+  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
+  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+  const int s0 = int(blockIdx.z) * g.per, s1 = min(s0 + g.per, (g.K + kStep - 1) / kStep);
+  int lo = 0, hi = 0;
+  if constexpr (MASK) token_range(g.tokens, lo, hi);
+  f32x4 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  SA sa;
+  SB sb;
+  auto load = [&](int s) {
+    sa.template load<MASK>(g.a, m0, s * kStep, g.K, g.tokens, lo, hi);
+    sb.template load<MASK>(g.b, n0, s * kStep, g.K, g.tokens, lo, hi);
+  };
+  if (s0 < s1) load(s0);
+  for (int s = s0; s < s1; ++s) {
+    __syncthreads();
+    sa.store(la);
+    sb.store(lb);
+    __syncthreads();
+    if (s + 1 < s1) load(s + 1);
+#pragma unroll
+    for (int kk = 0; kk < kStep; kk += 32) {
+      uint4 fa[PA][2], fb[PB][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+          fa[p][i] = *reinterpret_cast<const uint4 *>(&la[p][wm + i * 16 + lr][kk + lg * 8]);
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+          fb[p][i] = *reinterpret_cast<const uint4 *>(&lb[p][wn + i * 16 + lr][kk + lg * 8]);
+      }
+#pragma unroll
+      for (int p = PA - 1; p >= 0; --p)
+#pragma unroll
+        for (int q = PB - 1; q >= 0; --q)
+          if (p + q <= 2)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if constexpr (NATIVE)
+                  acc[i][j] = mfma_f16(__builtin_bit_cast(f16x8, fb[q][j]), __builtin_bit_cast(f16x8, fa[p][i]),
+                                       acc[i][j]);
+                else
+                  acc[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, fb[q][j]), __builtin_bit_cast(bf16x8, fa[p][i]),
+                                        acc[i][j]);
+              }
+    }
+  }
+  float *out = g.out + int64_t(blockIdx.z) * g.part;
+  const int N = g.b.rows;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = m0 + wm + i * 16 + lr;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int n = n0 + wn + j * 16 + 4 * lg;
+      if (m >= g.a.rows || n >= N) continue;
+      float v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = acc[i][j][c] + (g.bias && n + c < N ? g.bias[n + c] : 0.f);
+      float *p = out + int64_t(m) * N + n;
+      if (N % 4 == 0) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n + c < N) p[c] = v[c];
+      }
+    }
+  }
+}
+
+// ---- rows of logits ---------------------------------------------------------
+
+// Sequence of token t: the last b with off[b] <= t (0 without offsets), kept
+// inside [0, n).
+__device__ __forceinline__ int sequence_of(const Tokens &k, int t) {
+  if (!k.off) return 0;
+  int lo = 0, hi = k.n;  // off[lo] <= t < off[hi], for tokens inside
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (k.off[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct RowArgs {
+  Tokens tokens;
+  int E, K;
+  const float *parts;      // [z][T][E] partial logits, or null: `logits` holds them
+  int z;
+  const float *bias;       // added to the parts
+  float *logits;           // [T][E]
+  const int32_t *idx;      // [T][K]
+  // forward: one record per (chunk of tokens, sequence), at chunk + sequence
+  float *psum;             // [slots][E]
+  int32_t *count;          // [slots][E]
+  int32_t *ntok;           // [slots]
+  // backward
+  const int32_t *counts, *seq_tokens;  // [n][E], [n]
+  const float *dloss;
+  const float *dtopk;      // [T][K] or null
+  int renorm;
+  float *dl;               // [T][ld]
+  int ld;
+  float *dbias;            // [chunks][E] partial sums, or null
+};
+
+// Experts lane, lane + 64, ... of one token's logits; -inf past the end.
+template <int EPL>
+__device__ __forceinline__ void load_row(const RowArgs &a, int t, float (&l)[EPL]) {
+  const int lane = lane_id();
+  const int64_t at = int64_t(t) * a.E;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + kWave * i;
+    l[i] = -INFINITY;
+    if (e < a.E) {
+      if (a.parts) {
+        float s = 0.f;
+        for (int z = 0; z < a.z; ++z) s += a.parts[int64_t(z) * a.tokens.T * a.E + at + e];
+        l[i] = s + (a.bias ? a.bias[e] : 0.f);
+        a.logits[at + e] = l[i];
+      } else {
+        l[i] = a.logits[at + e];
+      }
+    }
+  }
+}
+template <int EPL>
+__device__ __forceinline__ void softmax_row(float (&l)[EPL]) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+  m = wave_max(m);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    l[i] = expf(l[i] - m);
+    s += l[i];
+  }
+  const float r = 1.0f / wave_sum(s);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] *= r;
+}
+
+// Forward: a wave takes kChunkTokens consecutive tokens and leaves, for every
+// sequence among them, the sums of its counted tokens' probabilities and the
+// counts of their slots.
+template <int EPL>
+__global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
+  const int chunk = int(blockIdx.x) * (kThreads / kWave) + int(threadIdx.x) / kWave;
+  const int t0 = chunk * kChunkTokens, t1 = min(t0 + kChunkTokens, a.tokens.T);
+  if (t0 >= t1) return;
+  const int lane = lane_id();
+  int lo, hi;
+  token_range(a.tokens, lo, hi);
+  float sum[EPL];
+  int32_t cnt[EPL], n = 0;
+  auto reset = [&]() {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
+    n = 0;
+  };
+  auto flush = [&](int b) {
+    const int64_t at = int64_t(chunk + b) * a.E;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + kWave * i;
+      if (e < a.E) a.psum[at + e] = sum[i], a.count[at + e] = cnt[i];
+    }
+    if (lane == 0) a.ntok[chunk + b] = n;
+  };
+  reset();
+  int b = -1;
+  for (int t = t0; t < t1; ++t) {
+    float l[EPL];
+    load_row<EPL>(a, t, l);
+    if (t < lo || t >= hi) continue;
+    const int tb = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t));
+    if (tb != b) {
+      if (b >= 0) flush(b), reset();
+      b = tb;
+    }
+    if (a.tokens.mask && !a.tokens.mask[t]) continue;
+    softmax_row<EPL>(l);
+    ++n;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum[i] += l[i];
+    for (int j = 0; j < a.K; ++j) {
+      const int e = a.idx[int64_t(t) * a.K + j];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) cnt[i] += e == lane + kWave * i && e < a.E;
+    }
+  }
+  if (b >= 0) flush(b);
+}
+
+struct FinishArgs {
+  Tokens tokens;
+  int E, K;
+  const float *psum;
+  const int32_t *count, *ntok;
+  int32_t *counts, *seq_tokens;
+  float *mean;
+  float *terms;   // [n][blocks of 64 experts]: sum of count * mean
+  float *loss;
+};
+
+constexpr int kFinishThreads = 1024;
+constexpr int kFinishRows = kFinishThreads / kWave;  // records summed side by side (16)
+
+// One sequence and 64 experts: the records of its chunks, 16 side by side.
+__global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(FinishArgs a) {
+  __shared__ float ps[kFinishRows][kWave];
+  __shared__ int32_t cs[kFinishRows][kWave], ns[kFinishRows];
+  const int b = blockIdx.y, lane = lane_id(), row = int(threadIdx.x) / kWave;
+  const int e = blockIdx.x * kWave + lane;
+  int lo = 0, hi = a.tokens.T;
+  if (a.tokens.off) {
+    lo = min(max(a.tokens.off[b], 0), a.tokens.T);
+    hi = min(max(a.tokens.off[b + 1], lo), a.tokens.T);
+  }
+  const int c0 = lo / kChunkTokens, c1 = hi > lo ? (hi - 1) / kChunkTokens + 1 : c0;
+  float p = 0.f;
+  int32_t c = 0, n = 0;
+#pragma unroll 8
+  for (int q = c0 + row; q < c1; q += kFinishRows) {
+    const int64_t at = int64_t(q + b) * a.E + min(e, a.E - 1);
+    p += a.psum[at];
+    c += a.count[at];
+    n += a.ntok[q + b];
+  }
+  ps[row][lane] = p, cs[row][lane] = c;
+  if (lane == 0) ns[row] = n;
+  __syncthreads();
+  if (row) return;
+#pragma unroll
+  for (int i = 1; i < kFinishRows; ++i) p += ps[i][lane], c += cs[i][lane], n += ns[i];
+  const float m = n ? p / float(n) : 0.f;
+  if (e < a.E) {
+    a.mean[int64_t(b) * a.E + e] = m;
+    a.counts[int64_t(b) * a.E + e] = c;
+  }
+  const float term = wave_sum(e < a.E ? float(c) * m : 0.f);
+  if (lane == 0) {
+    a.terms[b * gridDim.x + blockIdx.x] = term;
+    if (blockIdx.x == 0) a.seq_tokens[b] = n;
+  }
+}
+
+// The loss from the sequences' terms, one wave.
+__global__ __launch_bounds__(kWave) void balance_loss_kernel(FinishArgs a, int blocks) {
+  float s = 0.f;
+  int filled = 0;
+  for (int b = lane_id(); b < a.tokens.n; b += kWave) {
+    const int n = a.seq_tokens[b];
+    float v = 0.f;
+    for (int i = 0; i < blocks; ++i) v += a.terms[b * blocks + i];
+    if (n) s += v * (float(a.E) / (float(a.K) * float(n))), ++filled;
+  }
+  s = wave_sum(s);
+  const float f = wave_sum(float(filled));
+  if (lane_id() == 0) a.loss[0] = f > 0.f ? s / f : 0.f;
+}
+
+// Backward of the rows: dl of kChunkTokens tokens per wave, and their sum.
+template <int EPL>
+__global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
+  const int chunk = int(blockIdx.x) * (kThreads / kWave) + int(threadIdx.x) / kWave;
+  const int t0 = chunk * kChunkTokens, t1 = min(t0 + kChunkTokens, a.tokens.T);
+  if (t0 >= t1) return;
+  const int lane = lane_id();
+  int lo, hi;
+  token_range(a.tokens, lo, hi);
+  int filled = 0;
+  for (int b = lane; b < a.tokens.n; b += kWave) filled += a.seq_tokens[b] > 0;
+  const float nf = wave_sum(float(filled));
+  const float up = a.dloss ? a.dloss[0] : 1.0f;
+  float db[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) db[i] = 0.f;
+  for (int t = t0; t < t1; ++t) {
+    const bool on = t >= lo && t < hi && (!a.tokens.mask || a.tokens.mask[t]);
+    float d[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) d[i] = 0.f;
+    if (on) {
+      float p[EPL];
+      load_row<EPL>(a, t, p);
+      softmax_row<EPL>(p);
+      const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t));
+      const int n = a.seq_tokens[b];
+      const float fn = float(n);
+      // (a zero n or nf: no token of the forward pass counted; nothing flows)
+      const float coef = n > 0 && nf > 0.f ? up * float(a.E) / (float(a.K) * fn * fn * nf) : 0.f;
+      const int mean = int(int64_t(n) * a.K / a.E);
+      float g[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + kWave * i;
+        g[i] = e < a.E ? coef * float(a.counts[int64_t(b) * a.E + e] - mean) : 0.f;
+      }
+      // the routing weights' part, slot j in lane j
+      float add = 0.f;
+      int slot = -1;
+      if (a.dtopk) {
+        const bool has = lane < a.K;
+        slot = has ? a.idx[int64_t(t) * a.K + lane] : -1;
+        if (unsigned(slot) >= unsigned(a.E)) slot = -1;
+        const float dw = slot >= 0 ? a.dtopk[int64_t(t) * a.K + lane] : 0.f;
+        if (a.renorm) {
+          const float l = slot >= 0 ? a.logits[int64_t(t) * a.E + slot] : -INFINITY;
+          const float m = wave_max(l);
+          const float ex = slot >= 0 ? expf(l - m) : 0.f;
+          const float w = ex * (1.0f / wave_sum(ex));
+          const float s = wave_sum(slot >= 0 ? w * dw : 0.f);
+          add = slot >= 0 ? w * (dw - s) : 0.f;
+        } else {
+          add = dw;
+        }
+      }
+      auto scatter = [&](float (&to)[EPL]) {
+        for (int j = 0; j < a.K; ++j) {
+          const int e = read_lane_i(slot, j);
+          const float v = read_lane(add, j);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (e == lane + kWave * i) to[i] += v;
+        }
+      };
+      if (a.dtopk && !a.renorm) scatter(g);
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) s += p[i] * g[i];
+      s = wave_sum(s);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) d[i] = p[i] * (g[i] - s);
+      if (a.dtopk && a.renorm) scatter(d);
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + kWave * i;
+      if (e < a.ld) a.dl[int64_t(t) * a.ld + e] = d[i];
+      db[i] += d[i];
+    }
+  }
+  if (a.dbias) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + kWave * i;
+      if (e < a.E) a.dbias[int64_t(chunk) * a.E + e] = db[i];
+    }
+  }
+}
+
+// out[i] = sum over `parts` of p[part * n + i], in order.
+__global__ __launch_bounds__(kThreads) void sum_parts_kernel(const float *p, int parts, int64_t n, float *out) {
+  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= n) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int z = 0; z < parts; ++z) s += p[int64_t(z) * n + i];
+  out[i] = s;
+}
+
+// out[e] = sum over chunks of p[chunk][E], 64 experts per workgroup.
+__global__ __launch_bounds__(kFinishThreads) void sum_chunks_kernel(const float *p, int chunks, int E, float *out) {
+  __shared__ float ps[kFinishRows][kWave];
+  const int lane = lane_id(), row = int(threadIdx.x) / kWave, e = blockIdx.x * kWave + lane;
+  float s = 0.f;
+#pragma unroll 8
+  for (int c = row; c < chunks; c += kFinishRows) s += p[int64_t(c) * E + min(e, E - 1)];
+  ps[row][lane] = s;
+  __syncthreads();
+  if (row) return;
+#pragma unroll
+  for (int i = 1; i < kFinishRows; ++i) s += ps[i][lane];
+  if (e < E) out[e] = s;
+}
+
+int chunks_of(int32_t T) { return (T + kChunkTokens - 1) / kChunkTokens; }
+int tiles_of(int64_t n) { return int((n + kTile - 1) / kTile); }
+
+// Parts of a reduction of `steps` steps over `tiles` output tiles: enough
+// workgroups for the GPU's 256 CUs, at least `least` steps each.
+int parts_of(int64_t tiles, int steps, int want, int least) {
+  int z = 1;
+  while (tiles * z < want && steps >= 2 * z * least && z < 32) z *= 2;
+  return z;
+}
+int logit_parts(const moe_layer_desc *d, int32_t T) {
+  return parts_of(int64_t(tiles_of(T)) * tiles_of(d->n_experts), tiles_of(d->d_model), 256, 2);
+}
+int router_parts(const moe_layer_desc *d, int32_t T) {
+  return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T), 512, 4);
+}
+
+template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK>
+void launch_gemm(GemmArgs g, int parts, hipStream_t s) {
+  const int steps = (g.K + kStep - 1) / kStep;
+  g.per = (steps + parts - 1) / parts;
+  g.part = int64_t(g.a.rows) * g.b.rows;
+  launch((split_gemm_kernel<DTA, KCA, DTB, KCB, NATIVE, MASK>),
+         dim3(unsigned(tiles_of(g.b.rows)), unsigned(tiles_of(g.a.rows)), unsigned(parts)), dim3(kThreads), 0, s, g);
+}
+
+template <typename F>
+void by_experts(int E, F &&f) {
+  if (E <= 64) f(std::integral_constant<int, 1>{});
+  else if (E <= 128) f(std::integral_constant<int, 2>{});
+  else if (E <= 256) f(std::integral_constant<int, 4>{});
+  else if (E <= 512) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+template <typename F>
+void by_dtype(int dt, F &&f) {
+  if (dt == MOE_DT_BF16) f(std::integral_constant<int, kDtBF16>{});
+  else if (dt == MOE_DT_F16) f(std::integral_constant<int, kDtF16>{});
+  else f(std::integral_constant<int, kDtF32>{});
+}
+
+template <class T>
+T *at(void *ws, size_t off) {
+  return reinterpret_cast<T *>(static_cast<char *>(ws) + off);
+}
+
+Operand x_operand(const moe_layer_desc *d, int32_t T, const void *x, bool kc) {
+  return Operand{x, d->d_model, kc ? T : d->d_model, 1};  // d_model is a multiple of 8
+}
+
+}  // namespace
+
+BalanceWorkspace balance_workspace_layout(const moe_layer_desc *d, int32_t T, int32_t n_seqs) {
+  BalanceWorkspace b{};
+  const size_t E = d->n_experts, D = d->d_model, slots = size_t(chunks_of(T)) + n_seqs;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 255) & ~size_t(255);
+    return at;
+  };
+  const int zl = logit_parts(d, T);
+  b.parts = take(zl > 1 ? size_t(zl) * T * E * 4 : 0);
+  b.psum = take(slots * E * 4);
+  b.count = take(slots * E * 4);
+  b.ntok = take(slots * 4);
+  b.terms = take(size_t(n_seqs) * ((E + kWave - 1) / kWave) * 4);
+  const size_t fwd = o;
+  o = 0;
+  const int zw = router_parts(d, T);
+  b.ld = int((E + 3) / 4 * 4);
+  b.dl = take(size_t(T) * b.ld * 4);
+  b.dwp = take(zw > 1 ? size_t(zw) * D * E * 4 : 0);
+  b.dbp = take(size_t(chunks_of(T)) * E * 4);
+  b.total = std::max(std::max(fwd, o), size_t(256));
+  return b;
+}
+
+void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, const void *w_router, const float *bias,
+                         const int32_t *topk_idx, const uint8_t *mask, int32_t n_seqs, const int32_t *seq_off,
+                         float *logits, int32_t *counts, int32_t *seq_tokens, float *mean, float *loss, void *ws,
+                         void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int E = d->n_experts, D = d->d_model;
+  const BalanceWorkspace L = balance_workspace_layout(d, T, n_seqs);
+  const Tokens tk{mask, seq_off, n_seqs, T};
+  if (T > 0) {
+    const int z = logit_parts(d, T);
+    GemmArgs g{};
+    g.a = x_operand(d, T, x, true);
+    g.b = Operand{w_router, E, E, E % 4 == 0};
+    g.K = D;
+    g.out = z > 1 ? at<float>(ws, L.parts) : logits;
+    g.bias = z > 1 ? nullptr : bias;
+    by_dtype(d->act_dtype, [&](auto dt) {
+      constexpr int DT = decltype(dt)::value;
+      launch_gemm<DT, true, DT, false, DT == kDtF16, false>(g, z, s);
+    });
+    RowArgs r{};
+    r.tokens = tk, r.E = E, r.K = d->top_k;
+    r.parts = z > 1 ? at<float>(ws, L.parts) : nullptr, r.z = z, r.bias = bias;
+    r.logits = logits, r.idx = topk_idx;
+    r.psum = at<float>(ws, L.psum), r.count = at<int32_t>(ws, L.count), r.ntok = at<int32_t>(ws, L.ntok);
+    by_experts(E, [&](auto n) {
+      launch((balance_rows_kernel<decltype(n)::value>), dim3((chunks_of(T) + 3) / 4), dim3(kThreads), 0, s, r);
+    });
+  }
+  FinishArgs f{tk, E, d->top_k, at<float>(ws, L.psum), at<int32_t>(ws, L.count), at<int32_t>(ws, L.ntok),
+               counts, seq_tokens, mean, at<float>(ws, L.terms), loss};
+  const int blocks = (E + kWave - 1) / kWave;
+  launch(balance_finish_kernel, dim3(blocks, n_seqs), dim3(kFinishThreads), 0, s, f);
+  launch(balance_loss_kernel, dim3(1), dim3(kWave), 0, s, f, blocks);
+}
+
+void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, const void *w_router,
+                             const int32_t *topk_idx, const uint8_t *mask, int32_t n_seqs, const int32_t *seq_off,
+                             const float *logits, const int32_t *counts, const int32_t *seq_tokens,
+                             const float *dloss, const float *dtopk_w, float *dx, float *dw, float *dbias, void *ws,
+                             void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int E = d->n_experts, D = d->d_model;
+  const BalanceWorkspace L = balance_workspace_layout(d, T, n_seqs);
+  const Tokens tk{mask, seq_off, n_seqs, T};
+  float *dl = at<float>(ws, L.dl);
+  if (T > 0) {
+    RowArgs r{};
+    r.tokens = tk, r.E = E, r.K = d->top_k;
+    r.logits = const_cast<float *>(logits), r.idx = topk_idx;
+    r.counts = counts, r.seq_tokens = seq_tokens, r.dloss = dloss, r.dtopk = dtopk_w, r.renorm = d->renormalize;
+    r.dl = dl, r.ld = L.ld, r.dbias = dbias ? at<float>(ws, L.dbp) : nullptr;
+    by_experts(E, [&](auto n) {
+      launch((balance_dlogits_kernel<decltype(n)::value>), dim3((chunks_of(T) + 3) / 4), dim3(kThreads), 0, s, r);
+    });
+    if (dx) {
+      GemmArgs g{};
+      g.a = Operand{dl, L.ld, T, 1};
+      const int esz = int(act_bytes(d));
+      g.b = Operand{w_router, E, D, E % (16 / esz) == 0};
+      g.K = E, g.out = dx;
+      by_dtype(d->act_dtype, [&](auto dt) {
+        launch_gemm<kDtF32, true, decltype(dt)::value, true, false, false>(g, 1, s);
+      });
+    }
+  }
+  if (dw) {
+    const int z = router_parts(d, T);
+    GemmArgs g{};
+    g.a = x_operand(d, T, x, false);
+    g.b = Operand{dl, L.ld, E, 1};
+    g.K = T, g.out = z > 1 ? at<float>(ws, L.dwp) : dw;
+    g.tokens = tk;
+    by_dtype(d->act_dtype, [&](auto dt) {
+      launch_gemm<decltype(dt)::value, false, kDtF32, false, false, true>(g, z, s);
+    });
+    if (z > 1) {
+      const int64_t n = int64_t(D) * E;
+      launch(sum_parts_kernel, dim3(unsigned((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
+             static_cast<const float *>(g.out), z, n, dw);
+    }
+  }
+  if (dbias)
+    launch(sum_chunks_kernel, dim3((E + kWave - 1) / kWave), dim3(kFinishThreads), 0, s,
+           static_cast<const float *>(at<float>(ws, L.dbp)), T > 0 ? chunks_of(T) : 0, E, dbias);
+}
+
+}  // namespace moe

@@ -276,14 +276,69 @@ int moe_pack_weights(const moe_layer_desc *desc, int32_t proj, const void *w, co
   return hip_status();
 }
 
+namespace {
+// The arguments that the balance loss and its backward share.
+int validate_balance(const moe_layer_desc *d, int32_t T, const void *x, const void *w_router, const int32_t *topk_idx,
+                     const uint8_t *mask, int32_t n_seqs, const int32_t *seq_off, const void *ws, size_t ws_bytes) {
+  int s;
+  if ((s = validate_desc(d)) || (s = validate_T(T))) return s;
+  if (n_seqs < 1 || n_seqs > kMaxSeqs) return MOE_E_INVALID;
+  const bool none = T == 0;  // arrays of no tokens may have no address
+  if ((s = validate_ptr(x, none)) || (s = validate_ptr(w_router)) || (s = validate_ptr(topk_idx, none)) ||
+      (s = validate_ptr(mask, true)) || (s = validate_ptr(seq_off, n_seqs == 1)) || (s = validate_ptr(ws)))
+    return s;
+  return ws_bytes < balance_workspace_layout(d, T, n_seqs).total ? MOE_E_WORKSPACE : MOE_OK;
+}
+}  // namespace
+
+int moe_balance_workspace_size(const moe_layer_desc *desc, int32_t T, int32_t n_seqs, size_t *bytes) {
+  int s;
+  if ((s = validate_desc(desc)) || (s = validate_T(T))) return s;
+  if (!bytes || n_seqs < 1 || n_seqs > kMaxSeqs) return MOE_E_INVALID;
+  *bytes = balance_workspace_layout(desc, T, n_seqs).total;
+  return MOE_OK;
+}
+
+int moe_balance_loss(const moe_layer_desc *desc, int32_t T, const void *x, const void *w_router,
+                     const float *router_bias, const int32_t *topk_idx, const uint8_t *token_mask, int32_t n_seqs,
+                     const int32_t *seq_off, float *logits, int32_t *expert_counts, int32_t *seq_tokens,
+                     float *prob_mean, float *loss, void *ws, size_t ws_bytes, void *stream) {
+  int s;
+  if ((s = validate_balance(desc, T, x, w_router, topk_idx, token_mask, n_seqs, seq_off, ws, ws_bytes))) return s;
+  if ((s = validate_ptr(router_bias, true)) || (s = validate_ptr(logits, T == 0)) || (s = validate_ptr(expert_counts)) ||
+      (s = validate_ptr(seq_tokens)) || (s = validate_ptr(prob_mean)) || (s = validate_ptr(loss)))
+    return s;
+  launch_balance_loss(desc, T, x, w_router, router_bias, topk_idx, token_mask, n_seqs, seq_off, logits, expert_counts,
+                      seq_tokens, prob_mean, loss, ws, stream);
+  return hip_status();
+}
+
+int moe_balance_loss_backward(const moe_layer_desc *desc, int32_t T, const void *x, const void *w_router,
+                              const int32_t *topk_idx, const uint8_t *token_mask, int32_t n_seqs,
+                              const int32_t *seq_off, const float *logits, const int32_t *expert_counts,
+                              const int32_t *seq_tokens, const float *dloss, const float *dtopk_w, float *dx,
+                              float *dw_router, float *drouter_bias, void *ws, size_t ws_bytes, void *stream) {
+  int s;
+  if ((s = validate_balance(desc, T, x, w_router, topk_idx, token_mask, n_seqs, seq_off, ws, ws_bytes))) return s;
+  if ((s = validate_ptr(logits, T == 0)) || (s = validate_ptr(expert_counts)) || (s = validate_ptr(seq_tokens)) ||
+      (s = validate_ptr(dloss, true)) || (s = validate_ptr(dtopk_w, true)) || (s = validate_ptr(dx, true)) ||
+      (s = validate_ptr(dw_router, true)) || (s = validate_ptr(drouter_bias, true)))
+    return s;
+  if (!dx && !dw_router && !drouter_bias) return MOE_E_INVALID;
+  launch_balance_backward(desc, T, x, w_router, topk_idx, token_mask, n_seqs, seq_off, logits, expert_counts,
+                          seq_tokens, dloss, dtopk_w, dx, dw_router, drouter_bias, ws, stream);
+  return hip_status();
+}
+
 int moe_fp8_quantize(int32_t n_matrices, int32_t rows, int32_t cols, const void *x, int32_t dtype, int32_t block_rows,
                      uint8_t *codes, float *scales, void *stream) {
   int s;
   if (n_matrices < 0 || rows < 0 || cols <= 0 || cols % 16) return MOE_E_INVALID;
   if (!valid_dtype(dtype) || (block_rows != 1 && block_rows != 128)) return MOE_E_INVALID;
-  if ((s = validate_ptr(x)) || (s = validate_ptr(codes)) || (s = validate_ptr(scales))) return s;
   const int64_t all = int64_t(n_matrices) * rows, nbc = (cols + 127) / 128;
-  if (all == 0) return MOE_OK;
+  const bool none = all == 0;  // empty arrays may have no address
+  if ((s = validate_ptr(x, none)) || (s = validate_ptr(codes, none)) || (s = validate_ptr(scales, none))) return s;
+  if (none) return MOE_OK;
   const int64_t groups = block_rows == 1 ? (all + 31) / 32 * nbc : int64_t(n_matrices) * ((rows + 127) / 128) * nbc;
   if (all > INT32_MAX || groups > kMaxGroups) return MOE_E_INVALID;
   if (block_rows == 1) launch_fp8_rows(x, dtype, int32_t(all), cols, codes, scales, stream);
@@ -298,9 +353,10 @@ int moe_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_
   if (rows < 0 || a_rows < 0 || N <= 0 || K <= 0 || N % 16 || K % 16 || int64_t(N) * K > (int64_t(1) << 31))
     return MOE_E_INVALID;
   if (n_experts < 1 || n_experts > kMaxExperts || !valid_dtype(out_dtype)) return MOE_E_INVALID;
-  if ((s = validate_ptr(a)) || (s = validate_ptr(a_scales)) || (s = validate_ptr(row_map, true)) ||
+  const bool none = rows == 0;
+  if ((s = validate_ptr(a, none)) || (s = validate_ptr(a_scales, none)) || (s = validate_ptr(row_map, true)) ||
       (s = validate_ptr(expert_off, n_experts == 1)) || (s = validate_ptr(w)) || (s = validate_ptr(w_scales)) ||
-      (s = validate_ptr(y)))
+      (s = validate_ptr(y, none)))
     return s;
   if (rows == 0) return MOE_OK;
   if (a_rows < (row_map ? 1 : rows)) return MOE_E_INVALID;

@@ -335,6 +335,26 @@ void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, co
                            const moe_weights *w, const int32_t *counters, const PlanItem *tiles,
                            const FfnScratch &sc, float *y_sorted, void *stream, StageMarker *mk);
 
+// ---- balance loss -----------------------------------------------------------
+constexpr int kMaxSeqs = 4096;
+struct BalanceWorkspace {
+  size_t parts;                     // forward: [z][T][E] partial logits (z > 1)
+  size_t psum, count, ntok, terms;  // records per (chunk of tokens, sequence); loss terms
+  size_t dl, dwp, dbp;              // backward: [T][ld] logit gradients, [z][D][E] (z > 1), [chunks][E]
+  int ld;
+  size_t total;
+};
+BalanceWorkspace balance_workspace_layout(const moe_layer_desc *d, int32_t T, int32_t n_seqs);
+void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, const void *w_router, const float *bias,
+                         const int32_t *topk_idx, const uint8_t *mask, int32_t n_seqs, const int32_t *seq_off,
+                         float *logits, int32_t *counts, int32_t *seq_tokens, float *mean, float *loss, void *ws,
+                         void *stream);
+void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, const void *w_router,
+                             const int32_t *topk_idx, const uint8_t *mask, int32_t n_seqs, const int32_t *seq_off,
+                             const float *logits, const int32_t *counts, const int32_t *seq_tokens,
+                             const float *dloss, const float *dtopk_w, float *dx, float *dw, float *dbias, void *ws,
+                             void *stream);
+
 // Combine.
 // Combine of fp32 rows (ys_sh null), fp16 rows with exponents ys_sh, or
 // parts > 1 fp32 partial rows added in part order.

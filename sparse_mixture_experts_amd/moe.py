@@ -28,7 +28,8 @@ _ACT = {"swiglu": MOE_ACT_SWIGLU, "geglu": MOE_ACT_GEGLU}
 EXPORTED = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
             "moe_forward", "moe_forward_timed", "moe_backward_workspace_size", "moe_backward",
             "moe_status_string", "moe_forward_noalloc", "moe_packed_bytes", "moe_pack_weights",
-            "moe_fp8_quantize", "moe_fp8_matmul", "moe_fp8_transpose")
+            "moe_fp8_quantize", "moe_fp8_matmul", "moe_fp8_transpose",
+            "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward")
 MOE_PROJ_GATE, MOE_PROJ_UP, MOE_PROJ_GATE_UP, MOE_PROJ_DOWN = 0, 1, 2, 3
 _PROJ = {"gate": MOE_PROJ_GATE, "up": MOE_PROJ_UP, "gate_up": MOE_PROJ_GATE_UP, "down": MOE_PROJ_DOWN}
 NOALLOC_SCRATCH_BYTES = 96 * 1024 * 1024  # MOE_NOALLOC_SCRATCH_BYTES
@@ -84,6 +85,10 @@ def load() -> ctypes.CDLL:
         lib.moe_stream_read.argtypes = [vp, sz, vp, i32, vp]
         lib.moe_router_packed_bytes.argtypes = [P(LayerDesc), P(sz)]
         lib.moe_pack_router.argtypes = [P(LayerDesc), vp, vp, vp]
+        lib.moe_balance_workspace_size.argtypes = [P(LayerDesc), i32, i32, P(sz)]
+        lib.moe_balance_loss.argtypes = [P(LayerDesc), i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.moe_balance_loss_backward.argtypes = [P(LayerDesc), i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
+                                                  vp, vp, vp, sz, vp]
         lib.moe_fp8_quantize.argtypes = [i32, i32, i32, vp, i32, i32, vp, vp, vp]
         lib.moe_fp8_matmul.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp]
         lib.moe_fp8_transpose.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp]
@@ -236,6 +241,33 @@ def moe_pack_weights(desc, proj: int, w, scales, biases, w_packed, stream=None):
     `biases`) into `w_packed` (moe_packed_bytes bytes)."""
     _check(load().moe_pack_weights(ctypes.byref(desc), proj, _ptr(w), _ptr(scales), _ptr(biases), _ptr(w_packed),
                                    _stream(stream)), "moe_pack_weights")
+
+
+def moe_balance_workspace_size(desc: LayerDesc, T: int, n_seqs: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().moe_balance_workspace_size(ctypes.byref(desc), T, n_seqs, ctypes.byref(out)),
+           "moe_balance_workspace_size")
+    return out.value
+
+
+def moe_balance_loss(desc, T, x, w_router, router_bias, topk_idx, token_mask, n_seqs, seq_off, logits, expert_counts,
+                     seq_tokens, prob_mean, loss, ws, stream=None):
+    """The balance loss (fp32 [1]) of the routing topk_idx over n_seqs sequences of tokens, with the per-expert
+    counts and mean probabilities of each; logits [T][E] is kept for the backward pass."""
+    _check(load().moe_balance_loss(ctypes.byref(desc), T, _ptr(x), _ptr(w_router), _ptr(router_bias), _ptr(topk_idx),
+                                   _ptr(token_mask), n_seqs, _ptr(seq_off), _ptr(logits), _ptr(expert_counts),
+                                   _ptr(seq_tokens), _ptr(prob_mean), _ptr(loss), _ptr(ws), _nbytes(ws),
+                                   _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(desc, T, x, w_router, topk_idx, token_mask, n_seqs, seq_off, logits, expert_counts,
+                              seq_tokens, dloss, dtopk_w, dx, dw_router, drouter_bias, ws, stream=None):
+    """Gradients of dloss * loss + <dtopk_w, topk_w> for x, w_router and router_bias (fp32; None: not wanted)."""
+    _check(load().moe_balance_loss_backward(ctypes.byref(desc), T, _ptr(x), _ptr(w_router), _ptr(topk_idx),
+                                            _ptr(token_mask), n_seqs, _ptr(seq_off), _ptr(logits),
+                                            _ptr(expert_counts), _ptr(seq_tokens), _ptr(dloss), _ptr(dtopk_w),
+                                            _ptr(dx), _ptr(dw_router), _ptr(drouter_bias), _ptr(ws), _nbytes(ws),
+                                            _stream(stream)), "moe_balance_loss_backward")
 
 
 def moe_fp8_quantize(n_matrices, rows, cols, x, dtype, block_rows, codes, scales, stream=None):
