@@ -13,10 +13,10 @@
 // 128 (of both operands), so each 16-byte load of a wave covers whole 64-byte
 // pieces of 16 rows.
 //
-// Two kernels.  The tile kernel (experts with many rows) takes 64 or 128
-// token rows by 256 weight rows: the rows' codes go through LDS, double
-// buffered, the weights straight from memory to the registers of the one wave
-// that uses them, a block ahead.  The decode kernel (few rows per expert) is
+// Three kernels.  The tile kernel (experts with many rows) takes 64 token
+// rows by 256 weight rows, the wide one 128 by 256: the rows' codes go through
+// LDS, double buffered, the weights straight from memory to the registers of
+// the one wave that uses them.  The decode kernel (few rows per expert) is
 // bound by the weights' bytes: the waves of a workgroup split the reduction,
 // each with several blocks of weights in flight, and add up through LDS.
 #include <algorithm>
@@ -167,49 +167,49 @@ __device__ __forceinline__ void store4(const Fp8Args &a, int64_t at, const fp8_a
   }
 }
 
-// RB: 16-row blocks of token rows per tile.  EXACT: see Fp8Operand.
-template <int RB, int MODE, bool EXACT>
-__device__ __forceinline__ void tile_body(const Fp8Args &a) {
-  constexpr int BM = RB * 16;
+// The 64-row tile.  Weights and rows are requested two blocks ahead of their
+// use, into two sets of registers: with one block in flight a workgroup
+// waited out a memory round trip per block.  EXACT: see Fp8Operand.
+template <int MODE, bool EXACT>
+__global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
+  constexpr int RB = 4, BM = RB * 16;
   constexpr int PPT = BM * kPieces / kThreads;      // 16-byte pieces of the rows per thread
   constexpr int NTH = MODE == kGated ? kNT / 2 : kNT;
   constexpr int COLS = kNW * NTH * 16;              // output columns per workgroup
   // weight scale blocks that a workgroup meets: 256 rows cover two; gated:
   // one of gate rows, and two of up rows when they start inside a block
   constexpr int NS = MODE == kGated ? 3 : 2;
-  constexpr int SPT = (BM * NS + kThreads - 1) / kThreads;
+  constexpr int NSL = kThreads / BM;                // one scale per thread (those past NS repeat the last)
+  static_assert(NS <= NSL, "one scale per thread");
   __shared__ __align__(16) uint8_t sa[2][BM][kRowBytes];
-  __shared__ float ss[2][NS][BM];                   // row scale * weight scale
+  __shared__ float ss[2][NSL][BM];                  // row scale * weight scale
   __shared__ float rmax[MODE == kGated ? kNW : 1][BM];
 
   const int nbx = (a.N + COLS - 1) / COLS;
   PlanItem tile;
   int bx;
   if (!my_work(a, BM, nbx, tile, bx)) return;
-  const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = lane_id();
   const int lr = lane & 15, lg = lane >> 4;
   const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
   const int col0 = (bx * kNW + wave) * NTH * 16;    // first output column of this wave
   const int n_rows = MODE == kGated && a.fused ? 2 * a.N : a.N;  // rows of one expert's matrix
   const int nbr = (n_rows + kFp8Block - 1) / kFp8Block;
 
-  // this lane's row of each weight tile (clamped; what a tile past the end
-  // computes is not stored)
+  // each weight tile's first row (clamped; what a tile past the end computes
+  // is not stored) and which of the NS scales it takes
   const uint8_t *wp[kNT];
-  int sidx[kNT];  // which of the NS scales
+  int sidx[kNT];
   const int up0 = MODE == kGated && a.fused ? a.N : 0;
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
     const bool up = MODE == kGated && nt >= NTH;
     const int col = min(col0 + (nt % NTH) * 16, a.N - 16);
     const int row = col + (up ? up0 : 0);
-    const uint8_t *base = up && !a.fused ? a.w1 : a.w0;
-    wp[nt] = base + (int64_t(tile.expert) * n_rows + row + lr) * K + lg * 16;
-    if (MODE == kGated)
-      sidx[nt] = up ? 1 + (row / kFp8Block - (up0 + bx * COLS) / kFp8Block) : 0;
-    else
-      sidx[nt] = min(col / kFp8Block - bx * (COLS / kFp8Block), 1);
-    sidx[nt] = __builtin_amdgcn_readfirstlane(max(sidx[nt], 0));
+    wp[nt] = (up && !a.fused ? a.w1 : a.w0) + (int64_t(tile.expert) * n_rows + row) * K;
+    const int blk = MODE == kGated ? (up ? 1 + row / kFp8Block - (up0 + bx * COLS) / kFp8Block : 0)
+                                   : col / kFp8Block - bx * (COLS / kFp8Block);
+    sidx[nt] = __builtin_amdgcn_readfirstlane(min(max(blk, 0), NS - 1));
   }
   // staging of the rows' codes: pass p of a thread -> row 32 p + tid / 8, piece tid % 8
   const int piece = tid % kPieces;
@@ -222,50 +222,45 @@ __device__ __forceinline__ void tile_body(const Fp8Args &a) {
     aok[p] = r >= 0;
     ap[p] = static_cast<const uint8_t *>(a.a) + int64_t(max(r, 0)) * K;
   }
-  // staging of the scales: value q of a thread -> scale q / BM, row q % BM
-  const float *sap[SPT], *swp[SPT];
-  bool sok[SPT];
-#pragma unroll
-  for (int q = 0; q < SPT; ++q) {
-    const int v = min(tid + q * kThreads, BM * NS - 1), m = v % BM, s = v / BM;
-    const int r = m < tile.rows ? source_row(a, tile.row0 + m) : -1;
-    sok[q] = r >= 0;
-    sap[q] = a.as + max(r, 0);
-    int blk;
-    if (MODE == kGated) blk = s == 0 ? bx * COLS / kFp8Block : (up0 + bx * COLS) / kFp8Block + s - 1;
-    else blk = bx * (COLS / kFp8Block) + s;
-    const float *base = MODE == kGated && s > 0 && !a.fused ? a.s1 : a.s0;
-    swp[q] = base + (int64_t(tile.expert) * nbr + min(blk, nbr - 1)) * nb;
+  // staging of the scales: thread -> scale tid / BM, row tid % BM
+  const int sm = tid % BM, sn = min(tid / BM, NS - 1);
+  const int srow = sm < tile.rows ? source_row(a, tile.row0 + sm) : -1;
+  const float *sap = a.as + max(srow, 0), *swp;
+  {
+    const int blk = MODE == kGated ? (sn == 0 ? bx * COLS / kFp8Block : (up0 + bx * COLS) / kFp8Block + sn - 1)
+                                   : bx * (COLS / kFp8Block) + sn;
+    const float *base = MODE == kGated && sn > 0 && !a.fused ? a.s1 : a.s0;
+    swp = base + (int64_t(tile.expert) * nbr + min(blk, nbr - 1)) * nb;
   }
 
-  uint4 stg[PPT];
-  float sst[SPT];
-  uint4 wn[kNT][2];
-  auto load = [&](int s) {
+  uint4 wq[2][kNT][2], stg[2][PPT];
+  float sga[2], sgw[2];
+  // (blocks past the end repeat the last one: those loads hit the cache, and
+  // keeping them keeps the waits of every step the same)
+  auto load_rows = [&](int s, int r) {
     s = min(s, nb - 1);
-    const int k0 = s * kFp8Block;
+    const int k = min(s * kFp8Block + piece * 16, K - 16);
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      wn[nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0, K - 16 - lg * 16));
-      wn[nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0 + 64, K - 16 - lg * 16));
-    }
-#pragma unroll
-    for (int p = 0; p < PPT; ++p) stg[p] = *reinterpret_cast<const uint4 *>(ap[p] + min(k0 + piece * 16, K - 16));
-#pragma unroll
-    for (int q = 0; q < SPT; ++q) sst[q] = sap[q][int64_t(s) * a.a_rows] * swp[q][s];
+    for (int p = 0; p < PPT; ++p) stg[r][p] = *reinterpret_cast<const uint4 *>(ap[p] + k);
+    sga[r] = sap[int64_t(s) * a.a_rows];
+    sgw[r] = swp[s];
   };
-  auto stage = [&](int s) {  // into buffer s % 2
-    const int buf = s & 1, k0 = s * kFp8Block;
+  auto load_weights = [&](int s, int r, int nt) {
+    const int k = min(s, nb - 1) * kFp8Block;
+    const uint32_t o0 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + lg * 16, K - 16));
+    const uint32_t o1 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + 64 + lg * 16, K - 16));
+    wq[r][nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + o0);
+    wq[r][nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + o1);
+  };
+  auto stage = [&](int s, int r) {  // block s from registers r into buffer r
+    const int k = s * kFp8Block + piece * 16;
 #pragma unroll
-    for (int p = 0; p < PPT; ++p) {
-      const int m = p * (kThreads / kPieces) + tid / kPieces;
-      *reinterpret_cast<uint4 *>(&sa[buf][m][piece * 16]) = keep(stg[p], aok[p] && k0 + piece * 16 < K);
-    }
-#pragma unroll
-    for (int q = 0; q < SPT; ++q) {
-      const int v = tid + q * kThreads;
-      if (v < BM * NS) ss[buf][v / BM][v % BM] = sok[q] ? sst[q] : 0.f;
-    }
+    for (int p = 0; p < PPT; ++p)
+      *reinterpret_cast<uint4 *>(&sa[r][p * (kThreads / kPieces) + tid / kPieces][piece * 16]) =
+          keep(stg[r][p], aok[p] && k < K);
+    // (without a branch: one here lets the compiler move a step's sums past
+    // it, with all its products in registers until then)
+    ss[r][tid / BM][sm] = srow >= 0 ? sga[r] * sgw[r] : 0.f;
   };
 
   fp8_acc acc[kNT][RB];
@@ -274,33 +269,56 @@ __device__ __forceinline__ void tile_body(const Fp8Args &a) {
 #pragma unroll
     for (int mt = 0; mt < RB; ++mt) acc[nt][mt] = fp8_acc{0.f, 0.f, 0.f, 0.f};
 
-  load(0);
-  stage(0);
-  __syncthreads();
-  for (int s = 0; s < nb; ++s) {
-    const int buf = s & 1, k0 = s * kFp8Block;
+  auto step = [&](int s, auto rc) {
+    constexpr int r = decltype(rc)::value;
+    load_rows(s + 2, r);
     // the codes past the end of the reduction are zero in both operands (a
     // stray code may be a NaN, which a zero in the other operand keeps)
+    const int k0 = s * kFp8Block;
     const bool ok0 = k0 + lg * 16 < K, ok1 = k0 + 64 + lg * 16 < K;
-    auto codes = [&](int nt) { return Fp8Operand<EXACT>(join8(keep(wn[nt][0], ok0), keep(wn[nt][1], ok1))); };
-    const Fp8Operand<EXACT> w[kNT] = {codes(0), codes(1), codes(2), codes(3)};
-    load(s + 1);
 #pragma unroll
-    for (int mt = 0; mt < RB; ++mt) {
-      const uint8_t *row = &sa[buf][mt * 16 + lr][lg * 16];
-      const Fp8Operand<EXACT> x(
-          join8(*reinterpret_cast<const uint4 *>(row), *reinterpret_cast<const uint4 *>(row + 64)));
+    for (int np = 0; np < kNT; np += 2) {
+      const Fp8Operand<EXACT> w0(join8(keep(wq[r][np][0], ok0), keep(wq[r][np][1], ok1)));
+      const Fp8Operand<EXACT> w1(join8(keep(wq[r][np + 1][0], ok0), keep(wq[r][np + 1][1], ok1)));
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const float sc = ss[buf][sidx[nt]][mt * 16 + lr];
-        const fp8_acc d = fp8_product(w[nt], x);
+      for (int mt = 0; mt < RB; ++mt) {
+        const uint8_t *row = &sa[r][mt * 16 + lr][lg * 16];
+        const Fp8Operand<EXACT> x(
+            join8(*reinterpret_cast<const uint4 *>(row), *reinterpret_cast<const uint4 *>(row + 64)));
+        const fp8_acc d0 = fp8_product(w0, x), d1 = fp8_product(w1, x);
+        const float s0 = ss[r][sidx[np]][mt * 16 + lr], s1 = ss[r][sidx[np + 1]][mt * 16 + lr];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][mt][i] = __builtin_fmaf(d[i], sc, acc[nt][mt][i]);
+        for (int i = 0; i < 4; ++i) {
+          acc[np][mt][i] = __builtin_fmaf(d0[i], s0, acc[np][mt][i]);
+          acc[np + 1][mt][i] = __builtin_fmaf(d1[i], s1, acc[np + 1][mt][i]);
+        }
       }
+      // (the loads stay behind the last use of the registers that they fill)
+      __builtin_amdgcn_sched_barrier(0);
+      load_weights(s + 2, r, np);
+      load_weights(s + 2, r, np + 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (s + 1 < nb) stage(s + 1);
+    stage(s + 1, 1 - r);
     __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using R0 = std::integral_constant<int, 0>;
+  using R1 = std::integral_constant<int, 1>;
+  load_rows(0, 0);
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) load_weights(0, 0, nt);
+  load_rows(1, 1);
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) load_weights(1, 1, nt);
+  stage(0, 0);
+  __syncthreads();
+  int st = 0;
+  for (; st + 1 < nb; st += 2) {
+    step(st, R0{});
+    step(st + 1, R1{});
   }
+  if (st < nb) step(st, R0{});
 
   if constexpr (MODE == kPlain) {
 #pragma unroll
@@ -355,9 +373,132 @@ __device__ __forceinline__ void tile_body(const Fp8Args &a) {
   }
 }
 
-template <int RB, int MODE, bool EXACT>
-__global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
-  tile_body<RB, MODE, EXACT>(a);
+// The 128-row tile of the 8-bit instruction, for products that the matrix
+// cores bound.  128 token rows by 64 weight rows per wave are 32 products of
+// 32 cycles for 16 KB read from LDS and 8 KB from memory, so that with two
+// waves per SIMD neither path (128 and 64 bytes a cycle) is near its limit.
+// The rows go from memory to LDS without passing through registers; the 16
+// bytes of piece c of row m lie at place c ^ (m % 8) of the row, which puts
+// the pieces that 8 lanes read together on different banks.
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+__global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
+  constexpr int RB = 8, BM = RB * 16, PASS = BM * kPieces / kThreads;  // 4
+  __shared__ __align__(16) uint8_t sa0[BM * kFp8Block], sa1[BM * kFp8Block];
+  __shared__ float ss0[2][BM], ss1[2][BM];  // row scale * scale of either block of 128 weight rows
+
+  const int nbx = (a.N + kBN - 1) / kBN;
+  PlanItem tile;
+  int bx;
+  if (!my_work(a, BM, nbx, tile, bx)) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = lane_id();
+  const int lr = lane & 15, lg = lane >> 4;
+  const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
+  const int col0 = bx * kBN + wave * kNT * 16;
+  const int nbr = (a.N + kFp8Block - 1) / kFp8Block;
+  const uint8_t *wp[kNT];
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt)
+    wp[nt] = a.w0 + (int64_t(tile.expert) * a.N + min(col0 + nt * 16, a.N - 16)) * K;
+  // pass p: row 32 p + tid / 8, the piece that belongs at place tid % 8
+  const int piece = (lane % kPieces) ^ (lane / kPieces);
+  const uint8_t *ap[PASS];
+#pragma unroll
+  for (int p = 0; p < PASS; ++p) {
+    const int m = p * (kThreads / kPieces) + tid / kPieces;
+    const int r = m < tile.rows ? source_row(a, tile.row0 + m) : -1;
+    ap[p] = static_cast<const uint8_t *>(a.a) + int64_t(max(r, 0)) * K;
+  }
+  const int sm = tid % BM, sn = tid / BM;
+  const int srow = sm < tile.rows ? source_row(a, tile.row0 + sm) : -1;
+  const float *sap = a.as + max(srow, 0);
+  const float *swp = a.s0 + (int64_t(tile.expert) * nbr + min(bx * (kBN / kFp8Block) + sn, nbr - 1)) * nb;
+
+  uint4 w0[kNT][2], w1[kNT][2];
+  float sga, sgw;
+  auto load = [&](int s, uint8_t *buf, uint4 (&w)[kNT][2]) {
+    s = min(s, nb - 1);
+    const int k = s * kFp8Block;
+    const int ka = min(k + piece * 16, K - 16);
+#pragma unroll
+    for (int p = 0; p < PASS; ++p)
+      __builtin_amdgcn_global_load_lds((global_void *)(ap[p] + ka),
+                                       (lds_void *)(buf + (p * kNW + wave) * (kWave * 16)), 16, 0, 0);
+    const uint32_t o0 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + lg * 16, K - 16));
+    const uint32_t o1 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + 64 + lg * 16, K - 16));
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      w[nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + o0);
+      w[nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + o1);
+    }
+    sga = sap[int64_t(s) * a.a_rows];
+    sgw = swp[s];
+  };
+  auto stage_scale = [&](float (&ss)[2][BM]) { ss[sn][sm] = srow >= 0 ? sga * sgw : 0.f; };
+  fp8_acc acc[kNT][RB];
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) acc[nt][mt] = fp8_acc{0.f, 0.f, 0.f, 0.f};
+  const uint32_t x0 = uint32_t(lr) * kFp8Block + ((lg ^ (lr & 7)) * 16);
+  const uint32_t x1 = uint32_t(lr) * kFp8Block + (((lg + 4) ^ (lr & 7)) * 16);
+  // one block; TAIL: it reaches past the end of the reduction, where the
+  // codes count as zero in both operands (a stray one may be a NaN)
+  auto block = [&](int s, const uint8_t *buf, const float (&ss)[2][BM], const uint4 (&w)[kNT][2], auto tail) {
+    constexpr bool TAIL = decltype(tail)::value;
+    const bool ok0 = s * kFp8Block + lg * 16 < K, ok1 = s * kFp8Block + 64 + lg * 16 < K;
+    auto codes = [&](const uint4 &lo, const uint4 &hi) {
+      return Fp8Operand<false>(TAIL ? join8(keep(lo, ok0), keep(hi, ok1)) : join8(lo, hi));
+    };
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) {
+      const Fp8Operand<false> x = codes(*reinterpret_cast<const uint4 *>(buf + x0 + mt * 16 * kFp8Block),
+                                        *reinterpret_cast<const uint4 *>(buf + x1 + mt * 16 * kFp8Block));
+      const float sc = ss[wave / 2][mt * 16 + lr];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const fp8_acc d = fp8_product(codes(w[nt][0], w[nt][1]), x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][mt][i] = __builtin_fmaf(d[i], sc, acc[nt][mt][i]);
+      }
+    }
+  };
+  const int whole = K / kFp8Block;  // blocks without a tail
+  load(0, sa0, w0);
+  stage_scale(ss0);
+  __syncthreads();
+  int s = 0;
+  for (; s + 1 < whole; s += 2) {
+    load(s + 1, sa1, w1);
+    block(s, sa0, ss0, w0, std::false_type{});
+    stage_scale(ss1);
+    __syncthreads();
+    load(s + 2, sa0, w0);
+    block(s + 1, sa1, ss1, w1, std::false_type{});
+    stage_scale(ss0);
+    __syncthreads();
+  }
+  // at most two blocks are left, the last perhaps short
+  if (s < nb) {
+    load(s + 1, sa1, w1);
+    block(s, sa0, ss0, w0, std::true_type{});
+    stage_scale(ss1);
+    __syncthreads();
+    if (s + 1 < nb) block(s + 1, sa1, ss1, w1, std::true_type{});
+  }
+#pragma unroll
+  for (int mt = 0; mt < RB; ++mt) {
+    const int m = mt * 16 + lr;
+    if (m < tile.rows) {
+      const bool ok = source_row(a, tile.row0 + m) >= 0;
+      const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+        if (col0 + nt * 16 < a.N)
+          store4(a, at + col0 + nt * 16, ok ? acc[nt][mt] : fp8_acc{0.f, 0.f, 0.f, 0.f});
+    }
+  }
 }
 
 // The decode kernel: 16 token rows by WN weight tiles per wave; KW of the
@@ -519,11 +660,15 @@ int64_t most_tiles(int64_t rows, int experts, int bm) {
   return rows / bm + std::min<int64_t>(rows, experts);
 }
 
-template <int RB, int MODE, bool EXACT>
+template <int MODE, bool EXACT>
 void launch_tile(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   constexpr int COLS = MODE == kGated ? kBN / 2 : kBN;
   const int64_t nbx = (a.N + COLS - 1) / COLS;
-  launch((fp8_tile_kernel<RB, MODE, EXACT>), dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
+  launch((fp8_tile_kernel<MODE, EXACT>), dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
+}
+void launch_wide(const Fp8Args &a, int64_t tiles, hipStream_t s) {
+  const int64_t nbx = (a.N + kBN - 1) / kBN;
+  launch(fp8_wide_kernel, dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
 }
 
 template <int KW, int WN, int MODE, int SRC>
@@ -589,9 +734,9 @@ void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, in
   const int bm = fp8_tile_rows(rows, n_experts, exact);
   const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
   if (bm == 16) launch_decode<kPlain, kSrcCodes>(g, tiles, s);
-  else if (exact) launch_tile<4, kPlain, true>(g, tiles, s);
-  else if (bm == 64) launch_tile<4, kPlain, false>(g, tiles, s);
-  else launch_tile<8, kPlain, false>(g, tiles, s);
+  else if (exact) launch_tile<kPlain, true>(g, tiles, s);
+  else if (bm == 64) launch_tile<kPlain, false>(g, tiles, s);
+  else launch_wide(g, tiles, s);
 }
 
 // Workspace of the expert FFN: x codes and scales (tile kernels), h as codes
@@ -637,9 +782,9 @@ void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, co
   if (mk) mk->mark("x_fp8");
   g.a = xq, g.as = xs, g.hs = hs;
   n.as = hs;
-  launch_tile<4, kGated, true>(g, max_tiles, s);
+  launch_tile<kGated, true>(g, max_tiles, s);
   if (mk) mk->mark("gateup_fp8");
-  launch_tile<4, kPlain, true>(n, max_tiles, s);
+  launch_tile<kPlain, true>(n, max_tiles, s);
   if (mk) mk->mark("down_fp8");
 }
 
