@@ -62,6 +62,16 @@ __device__ __forceinline__ float max8_lanes(float v) {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float fp8_acc __attribute__((ext_vector_type(4)));
 
+// Eight codes as fp16.
+__device__ __forceinline__ uint4 fp8_to_f16(uint32_t a, uint32_t b) {
+  const h2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false),
+                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true),
+                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false),
+                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true)};
+  return make_uint4(__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
+                    __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3]));
+}
+
 // The 32 codes of a 128-element block that a lane holds as an operand of one
 // 16x16 tile: row (operand a) or column (operand b) lane % 16.  The lane's
 // four results are rows 4 * (lane / 16) + i of column lane % 16.  Any
@@ -86,15 +96,12 @@ struct Fp8Operand {
 template <>
 struct Fp8Operand<true> {
   f16x8 v[4];
+  __device__ __forceinline__ Fp8Operand(const uint4 &a, const uint4 &b, const uint4 &c, const uint4 &d)
+      : v{__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, c),
+          __builtin_bit_cast(f16x8, d)} {}
   __device__ __forceinline__ explicit Fp8Operand(const i32x8 &c) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * j], 1.0f, false);
-      const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * j], 1.0f, true);
-      const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * j + 1], 1.0f, false);
-      const h2 e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[2 * j + 1], 1.0f, true);
-      v[j] = f16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
-    }
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(f16x8, fp8_to_f16(c[2 * j], c[2 * j + 1]));
   }
 };
 template <bool EXACT>

@@ -32,8 +32,53 @@ constexpr int kThreads = 256;
 constexpr int kNW = kThreads / kWave;
 constexpr int kNT = 4;                    // 16-row weight tiles per wave of the tile kernel
 constexpr int kBN = kNW * kNT * 16;       // weight rows per workgroup (256)
-constexpr int kRowBytes = kFp8Block + 16; // LDS row: 16 rows' 16-byte pieces fall into 16 different bank groups
 constexpr int kPieces = kFp8Block / 16;   // 16-byte pieces per row and block (8)
+
+__device__ __forceinline__ uint4 keep(const uint4 &v, bool ok) {
+  return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
+}
+
+// 16 bytes per lane from memory to consecutive places of LDS (1 KB a wave).
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+__device__ __forceinline__ void to_lds(const uint8_t *src, uint8_t *dst) {
+  __builtin_amdgcn_global_load_lds((global_void *)src, (lds_void *)dst, 16, 0, 0);
+}
+// Rows of 128 codes in LDS: piece c (16 bytes) of row m lies at place
+// c ^ (m % 8), which puts the pieces that 8 lanes read together, one of 8
+// rows each, on different banks.  Byte offset of piece c of row m:
+__device__ __forceinline__ uint32_t piece_at(int m, int c) { return uint32_t(m * kFp8Block + ((c ^ (m & 7)) * 16)); }
+// A wave's 1 KB covers 8 rows; the piece that lane l brings for its place.
+__device__ __forceinline__ int piece_of_lane(int l) { return (l % kPieces) ^ (l / kPieces); }
+
+// One 16 x 128 tile of weight codes on its way from memory to the operand
+// layout.  Loaded as it lies in memory (8 lanes to the 128 bytes of a row, so
+// that an instruction meets 8 cache lines; in the operand's own layout
+// neighbouring lanes are in different rows, and each load met 64), it is
+// turned around through a piece of LDS that only this wave uses.
+constexpr int kTileBytes = 16 * kFp8Block;
+struct WeightTile {
+  uint4 v[2];
+  // base: the tile's first row; k0: the block's first code.  Past the end of
+  // the reduction the codes are zero (a stray one may be a NaN).
+  __device__ __forceinline__ void load(const uint8_t *base, int K, int k0) {
+    const int lane = lane_id(), k = min(k0 + lane % kPieces * 16, K - 16);
+    const uint32_t o = uint32_t(lane / kPieces) * uint32_t(K) + uint32_t(k);
+    v[0] = *reinterpret_cast<const uint4 *>(base + o);
+    v[1] = *reinterpret_cast<const uint4 *>(base + 8 * int64_t(K) + o);
+  }
+  __device__ __forceinline__ void put(uint8_t *lds, int K, int k0) const {
+    const int lane = lane_id(), m = lane / kPieces, c = lane % kPieces;
+    const bool ok = k0 + c * 16 < K;
+    *reinterpret_cast<uint4 *>(lds + piece_at(m, c)) = keep(v[0], ok);
+    *reinterpret_cast<uint4 *>(lds + piece_at(m + 8, c)) = keep(v[1], ok);
+  }
+};
+__device__ __forceinline__ i32x8 tile_operand(const uint8_t *lds) {
+  const int lr = lane_id() & 15, lg = lane_id() >> 4;
+  return join8(*reinterpret_cast<const uint4 *>(lds + piece_at(lr, lg)),
+               *reinterpret_cast<const uint4 *>(lds + piece_at(lr, lg + 4)));
+}
 
 // What a projection writes: the product, or the gated unit of two of them
 // (as e4m3 codes per 128 columns from the tile kernel, as fp32 from the
@@ -63,73 +108,63 @@ struct Fp8Args {
   float *hs;                 // gated tile kernel: h scales [ceil(N/128)][rows]
 };
 
-// Tile `id` of BM rows over the experts' row ranges, and the number of tiles.
-// Ranges are clamped to [0, rows]; every lane of the wave takes part.
-__device__ __forceinline__ bool find_tile(const Fp8Args &a, int bm, int id, PlanItem &t, int &total) {
-  const int lane = lane_id();
-  const int per = (a.E + kWave - 1) / kWave;
-  const int e0 = lane * per, e1 = min(e0 + per, a.E);
-  auto range = [&](int e, int &lo, int &hi) {
-    lo = min(max(a.expert_off[e], 0), a.rows);
-    hi = min(max(a.expert_off[e + 1], lo), a.rows);
-  };
-  int n = 0;
-  for (int e = e0; e < e1; ++e) {
-    int lo, hi;
-    range(e, lo, hi);
-    n += (hi - lo + bm - 1) / bm;
-  }
-  const int incl = wave_incl_scan(n);
-  total = read_lane_i(incl, kWave - 1);
-  if (id >= total) return false;
-  int at = incl - n, fe = 0, frow = 0, frows = 0;
-  if (id >= at && id < incl) {
-    for (int e = e0; e < e1; ++e) {
-      int lo, hi;
-      range(e, lo, hi);
-      const int k = (hi - lo + bm - 1) / bm;
-      if (id < at + k) {
-        fe = e;
-        frow = lo + (id - at) * bm;
-        frows = min(bm, hi - frow);
-        break;
-      }
-      at += k;
-    }
-  }
-  const int src = __builtin_ctzll(__ballot(incl > id));
-  t.expert = read_lane_i(fe, src);
-  t.row0 = read_lane_i(frow, src);
-  t.rows = read_lane_i(frows, src);
-  return true;
-}
-
-// Number of row tiles of this call.
-__device__ __forceinline__ int count_tiles(const Fp8Args &a, int bm) {
-  if (a.tiles) return a.counters[1];
-  if (!a.expert_off) return (a.rows + bm - 1) / bm;
-  PlanItem t;
-  int total;
-  find_tile(a, bm, 0x7fffffff, t, total);
-  return total;
-}
-
 // This workgroup's row tile and column block (false: none is left).  Each
 // XCD takes one contiguous range of the work, ordered in groups of 8 column
 // blocks with the tiles of an expert together, so that what neighbours share
 // (a tile's rows, an expert's weights) is read into one L2.
+//
+// Without a plan the tiles are found here, by every wave: the experts' rows
+// in tiles of bm are counted 64 at a time, one prefix sum gives the number of
+// tiles, and the lane whose range holds this one's number looks it up.
+// Ranges are read as if clamped to [0, rows].
 __device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanItem &t, int &bx) {
-  const int n_tiles = count_tiles(a, bm);
+  const int lin = int(blockIdx.x), lane = lane_id();
+  int n_tiles, incl = 0, n = 0, e0 = 0, e1 = 0;
+  auto range = [&](int e, int &lo, int &hi) {
+    lo = min(max(a.expert_off[e], 0), a.rows);
+    hi = min(max(a.expert_off[e + 1], lo), a.rows);
+  };
+  if (a.tiles) {
+    n_tiles = a.counters[1];
+  } else if (a.expert_off) {
+    const int per = (a.E + kWave - 1) / kWave;
+    e0 = lane * per, e1 = min(e0 + per, a.E);
+    for (int e = e0; e < e1; ++e) {
+      int lo, hi;
+      range(e, lo, hi);
+      n += (hi - lo + bm - 1) / bm;
+    }
+    incl = wave_incl_scan(n);
+    n_tiles = read_lane_i(incl, kWave - 1);
+  } else {
+    n_tiles = (a.rows + bm - 1) / bm;
+  }
   const int work = n_tiles * nbx;  // the grid has at least as many workgroups
-  const int lin = int(blockIdx.x);
   if (lin >= work) return false;
   int tile;
   item_tile_block(xcd_contiguous(lin, work), n_tiles, nbx, min(nbx, kColGroup), tile, bx);
   if (a.tiles) {
     t = a.tiles[tile];
   } else if (a.expert_off) {
-    int total;
-    find_tile(a, bm, tile, t, total);
+    int at = incl - n, fe = 0, frow = 0, frows = 0;
+    if (tile >= at && tile < incl) {
+      for (int e = e0; e < e1; ++e) {
+        int lo, hi;
+        range(e, lo, hi);
+        const int k = (hi - lo + bm - 1) / bm;
+        if (tile < at + k) {
+          fe = e;
+          frow = lo + (tile - at) * bm;
+          frows = min(bm, hi - frow);
+          break;
+        }
+        at += k;
+      }
+    }
+    const int src = __builtin_ctzll(__ballot(incl > tile));
+    t.expert = read_lane_i(fe, src);
+    t.row0 = read_lane_i(frow, src);
+    t.rows = read_lane_i(frows, src);
   } else {
     t.expert = 0;
     t.row0 = tile * bm;
@@ -147,10 +182,6 @@ __device__ __forceinline__ int source_row(const Fp8Args &a, int p) {
   if (a.T && p >= a.n_routed) r = (p - a.n_routed) % a.T;
   else if (a.row_map) r = a.row_map[p];
   return unsigned(r) < unsigned(a.a_rows) ? r : -1;
-}
-
-__device__ __forceinline__ uint4 keep(const uint4 &v, bool ok) {
-  return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
 }
 
 // Four consecutive outputs of one row.
@@ -173,6 +204,11 @@ __device__ __forceinline__ void store4(const Fp8Args &a, int64_t at, const fp8_a
 template <int MODE, bool EXACT>
 __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
   constexpr int RB = 4, BM = RB * 16;
+  constexpr int NP = 2;                             // weight tiles that a read of the rows serves
+  // rows in LDS: codes, or (EXACT) fp16, turned into it once here instead of
+  // by every wave for every weight tile; 16 bytes of padding put the pieces
+  // that 16 lanes read together, one of 16 rows each, on different banks
+  constexpr int XB = EXACT ? 2 : 1, ROW = kFp8Block * XB + 16;
   constexpr int PPT = BM * kPieces / kThreads;      // 16-byte pieces of the rows per thread
   constexpr int NTH = MODE == kGated ? kNT / 2 : kNT;
   constexpr int COLS = kNW * NTH * 16;              // output columns per workgroup
@@ -181,7 +217,8 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
   constexpr int NS = MODE == kGated ? 3 : 2;
   constexpr int NSL = kThreads / BM;                // one scale per thread (those past NS repeat the last)
   static_assert(NS <= NSL, "one scale per thread");
-  __shared__ __align__(16) uint8_t sa[2][BM][kRowBytes];
+  __shared__ __align__(16) uint8_t sa[2][BM][ROW];
+  __shared__ __align__(16) uint8_t turn[kNW][kNT][kTileBytes];
   __shared__ float ss[2][NSL][BM];                  // row scale * weight scale
   __shared__ float rmax[MODE == kGated ? kNW : 1][BM];
 
@@ -233,7 +270,8 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
     swp = base + (int64_t(tile.expert) * nbr + min(blk, nbr - 1)) * nb;
   }
 
-  uint4 wq[2][kNT][2], stg[2][PPT];
+  WeightTile wq[2][kNT];
+  uint4 stg[2][PPT];
   float sga[2], sgw[2];
   // (blocks past the end repeat the last one: those loads hit the cache, and
   // keeping them keeps the waits of every step the same)
@@ -245,19 +283,19 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
     sga[r] = sap[int64_t(s) * a.a_rows];
     sgw[r] = swp[s];
   };
-  auto load_weights = [&](int s, int r, int nt) {
-    const int k = min(s, nb - 1) * kFp8Block;
-    const uint32_t o0 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + lg * 16, K - 16));
-    const uint32_t o1 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + 64 + lg * 16, K - 16));
-    wq[r][nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + o0);
-    wq[r][nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + o1);
+  auto load_weights = [&](int s, int r) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) wq[r][nt].load(wp[nt], K, min(s, nb - 1) * kFp8Block);
   };
   auto stage = [&](int s, int r) {  // block s from registers r into buffer r
     const int k = s * kFp8Block + piece * 16;
 #pragma unroll
-    for (int p = 0; p < PPT; ++p)
-      *reinterpret_cast<uint4 *>(&sa[r][p * (kThreads / kPieces) + tid / kPieces][piece * 16]) =
-          keep(stg[r][p], aok[p] && k < K);
+    for (int p = 0; p < PPT; ++p) {
+      const uint4 v = keep(stg[r][p], aok[p] && k < K);
+      uint4 *to = reinterpret_cast<uint4 *>(&sa[r][p * (kThreads / kPieces) + tid / kPieces][piece * 16 * XB]);
+      if constexpr (EXACT) to[0] = fp8_to_f16(v.x, v.y), to[1] = fp8_to_f16(v.z, v.w);
+      else to[0] = v;
+    }
     // (without a branch: one here lets the compiler move a step's sums past
     // it, with all its products in registers until then)
     ss[r][tid / BM][sm] = srow >= 0 ? sga[r] * sgw[r] : 0.f;
@@ -271,34 +309,34 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
 
   auto step = [&](int s, auto rc) {
     constexpr int r = decltype(rc)::value;
-    load_rows(s + 2, r);
-    // the codes past the end of the reduction are zero in both operands (a
-    // stray code may be a NaN, which a zero in the other operand keeps)
-    const int k0 = s * kFp8Block;
-    const bool ok0 = k0 + lg * 16 < K, ok1 = k0 + 64 + lg * 16 < K;
 #pragma unroll
-    for (int np = 0; np < kNT; np += 2) {
-      const Fp8Operand<EXACT> w0(join8(keep(wq[r][np][0], ok0), keep(wq[r][np][1], ok1)));
-      const Fp8Operand<EXACT> w1(join8(keep(wq[r][np + 1][0], ok0), keep(wq[r][np + 1][1], ok1)));
+    for (int nt = 0; nt < kNT; ++nt) wq[r][nt].put(turn[wave][nt], K, s * kFp8Block);
+    // (the loads stay behind the last use of the registers that they fill)
+    __builtin_amdgcn_sched_barrier(0);
+    load_rows(s + 2, r);
+    load_weights(s + 2, r);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int np = 0; np < kNT; np += NP) {
+      const Fp8Operand<EXACT> w0(tile_operand(turn[wave][np])), w1(tile_operand(turn[wave][np + NP - 1]));
 #pragma unroll
       for (int mt = 0; mt < RB; ++mt) {
-        const uint8_t *row = &sa[r][mt * 16 + lr][lg * 16];
-        const Fp8Operand<EXACT> x(
-            join8(*reinterpret_cast<const uint4 *>(row), *reinterpret_cast<const uint4 *>(row + 64)));
-        const fp8_acc d0 = fp8_product(w0, x), d1 = fp8_product(w1, x);
-        const float s0 = ss[r][sidx[np]][mt * 16 + lr], s1 = ss[r][sidx[np + 1]][mt * 16 + lr];
+        const uint4 *row = reinterpret_cast<const uint4 *>(&sa[r][mt * 16 + lr][lg * 16 * XB]);
+        const auto x = [&] {
+          if constexpr (EXACT) return Fp8Operand<true>(row[0], row[1], row[8], row[9]);
+          else return Fp8Operand<false>(join8(row[0], row[4]));
+        }();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[np][mt][i] = __builtin_fmaf(d0[i], s0, acc[np][mt][i]);
-          acc[np + 1][mt][i] = __builtin_fmaf(d1[i], s1, acc[np + 1][mt][i]);
+        for (int q = 0; q < NP; ++q) {
+          const fp8_acc d = fp8_product(q ? w1 : w0, x);
+          const float sc = ss[r][sidx[np + q]][mt * 16 + lr];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[np + q][mt][i] = __builtin_fmaf(d[i], sc, acc[np + q][mt][i]);
         }
+        if (EXACT && mt % 2) __builtin_amdgcn_sched_barrier(0);  // (more reads ahead would not fit the registers)
       }
-      // (the loads stay behind the last use of the registers that they fill)
-      __builtin_amdgcn_sched_barrier(0);
-      load_weights(s + 2, r, np);
-      load_weights(s + 2, r, np + 1);
-      __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_sched_barrier(0);
     stage(s + 1, 1 - r);
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
@@ -306,11 +344,9 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
   using R0 = std::integral_constant<int, 0>;
   using R1 = std::integral_constant<int, 1>;
   load_rows(0, 0);
-#pragma unroll
-  for (int nt = 0; nt < kNT; ++nt) load_weights(0, 0, nt);
+  load_weights(0, 0);
   load_rows(1, 1);
-#pragma unroll
-  for (int nt = 0; nt < kNT; ++nt) load_weights(1, 1, nt);
+  load_weights(1, 1);
   stage(0, 0);
   __syncthreads();
   int st = 0;
@@ -377,15 +413,11 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
 // cores bound.  128 token rows by 64 weight rows per wave are 32 products of
 // 32 cycles for 16 KB read from LDS and 8 KB from memory, so that with two
 // waves per SIMD neither path (128 and 64 bytes a cycle) is near its limit.
-// The rows go from memory to LDS without passing through registers; the 16
-// bytes of piece c of row m lie at place c ^ (m % 8) of the row, which puts
-// the pieces that 8 lanes read together on different banks.
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void global_void;
-
+// The rows go from memory to LDS without passing through registers.
 __global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
   constexpr int RB = 8, BM = RB * 16, PASS = BM * kPieces / kThreads;  // 4
   __shared__ __align__(16) uint8_t sa0[BM * kFp8Block], sa1[BM * kFp8Block];
+  __shared__ __align__(16) uint8_t turn[kNW][kNT][kTileBytes];
   __shared__ float ss0[2][BM], ss1[2][BM];  // row scale * scale of either block of 128 weight rows
 
   const int nbx = (a.N + kBN - 1) / kBN;
@@ -402,7 +434,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
   for (int nt = 0; nt < kNT; ++nt)
     wp[nt] = a.w0 + (int64_t(tile.expert) * a.N + min(col0 + nt * 16, a.N - 16)) * K;
   // pass p: row 32 p + tid / 8, the piece that belongs at place tid % 8
-  const int piece = (lane % kPieces) ^ (lane / kPieces);
+  const int piece = piece_of_lane(lane);
   const uint8_t *ap[PASS];
 #pragma unroll
   for (int p = 0; p < PASS; ++p) {
@@ -415,22 +447,148 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
   const float *sap = a.as + max(srow, 0);
   const float *swp = a.s0 + (int64_t(tile.expert) * nbr + min(bx * (kBN / kFp8Block) + sn, nbr - 1)) * nb;
 
-  uint4 w0[kNT][2], w1[kNT][2];
+  WeightTile wn[kNT];  // the next block's weights
+  i32x8 w[kNT];        // this one's, as operands
   float sga, sgw;
-  auto load = [&](int s, uint8_t *buf, uint4 (&w)[kNT][2]) {
+  auto load = [&](int s, uint8_t *buf) {
     s = min(s, nb - 1);
     const int k = s * kFp8Block;
     const int ka = min(k + piece * 16, K - 16);
 #pragma unroll
     for (int p = 0; p < PASS; ++p)
-      __builtin_amdgcn_global_load_lds((global_void *)(ap[p] + ka),
-                                       (lds_void *)(buf + (p * kNW + wave) * (kWave * 16)), 16, 0, 0);
-    const uint32_t o0 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + lg * 16, K - 16));
-    const uint32_t o1 = uint32_t(lr) * uint32_t(K) + uint32_t(min(k + 64 + lg * 16, K - 16));
+      to_lds(ap[p] + ka, buf + (p * kNW + wave) * (kWave * 16));
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      w[nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + o0);
-      w[nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + o1);
+    for (int nt = 0; nt < kNT; ++nt) wn[nt].load(wp[nt], K, k);
+    sga = sap[int64_t(s) * a.a_rows];
+    sgw = swp[s];
+  };
+  auto stage = [&](int s, float (&ss)[2][BM]) {  // block s: scales to LDS, weights through it
+    ss[sn][sm] = srow >= 0 ? sga * sgw : 0.f;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) wn[nt].put(turn[wave][nt], K, s * kFp8Block);
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) w[nt] = tile_operand(turn[wave][nt]);
+  };
+  fp8_acc acc[kNT][RB];
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) acc[nt][mt] = fp8_acc{0.f, 0.f, 0.f, 0.f};
+  const uint32_t x0 = piece_at(lr, lg), x1 = piece_at(lr, lg + 4);
+  // one block; TAIL: it reaches past the end of the reduction, where the
+  // rows' codes count as zero too
+  auto block = [&](int s, const uint8_t *buf, const float (&ss)[2][BM], auto tail) {
+    constexpr bool TAIL = decltype(tail)::value;
+    const bool ok0 = s * kFp8Block + lg * 16 < K, ok1 = s * kFp8Block + 64 + lg * 16 < K;
+    auto codes = [&](const uint4 &lo, const uint4 &hi) {
+      return Fp8Operand<false>(TAIL ? join8(keep(lo, ok0), keep(hi, ok1)) : join8(lo, hi));
+    };
+    auto rows = [&](int mt) {
+      return codes(*reinterpret_cast<const uint4 *>(buf + x0 + mt * 16 * kFp8Block),
+                   *reinterpret_cast<const uint4 *>(buf + x1 + mt * 16 * kFp8Block));
+    };
+    Fp8Operand<false> x = rows(0);
+    float sc = ss[wave / 2][lr];
+#pragma unroll
+    for (int mt = 0; mt < RB; ++mt) {
+      const Fp8Operand<false> xn = rows(mt + 1 < RB ? mt + 1 : mt);  // read while this one multiplies
+      const float scn = ss[wave / 2][(mt + 1 < RB ? mt + 1 : mt) * 16 + lr];
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const fp8_acc d = fp8_product(Fp8Operand<false>(w[nt]), x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][mt][i] = __builtin_fmaf(d[i], sc, acc[nt][mt][i]);
+      }
+      x = xn, sc = scn;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int whole = K / kFp8Block;  // blocks without a tail
+  load(0, sa0);
+  stage(0, ss0);
+  __syncthreads();
+  int s = 0;
+  for (; s + 1 < whole; s += 2) {
+    load(s + 1, sa1);
+    block(s, sa0, ss0, std::false_type{});
+    stage(s + 1, ss1);
+    __syncthreads();
+    load(s + 2, sa0);
+    block(s + 1, sa1, ss1, std::false_type{});
+    stage(s + 2, ss0);
+    __syncthreads();
+  }
+  // at most two blocks are left, the last perhaps short
+  if (s < nb) {
+    load(s + 1, sa1);
+    block(s, sa0, ss0, std::true_type{});
+    stage(s + 1, ss1);
+    __syncthreads();
+    if (s + 1 < nb) block(s + 1, sa1, ss1, std::true_type{});
+  }
+#pragma unroll
+  for (int mt = 0; mt < RB; ++mt) {
+    const int m = mt * 16 + lr;
+    if (m < tile.rows) {
+      const bool ok = source_row(a, tile.row0 + m) >= 0;
+      const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+        if (col0 + nt * 16 < a.N)
+          store4(a, at + col0 + nt * 16, ok ? acc[nt][mt] : fp8_acc{0.f, 0.f, 0.f, 0.f});
+    }
+  }
+}
+
+// The 256-row tile, for large products: 8 waves of 128 token rows by 64
+// weight rows, both operands from memory to LDS without passing through
+// registers and read from there as they are used (24 KB for a wave's 32
+// products).  One workgroup fills a CU.
+constexpr int kHugeRows = 256;
+constexpr int kHugeThreads = 512;
+__global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
+  constexpr int RB = 8, BM = kHugeRows, PASS = BM * kPieces / kHugeThreads;  // 4
+  __shared__ __align__(16) uint8_t sa0[BM * kFp8Block], sa1[BM * kFp8Block];
+  __shared__ __align__(16) uint8_t sw0[kBN * kFp8Block], sw1[kBN * kFp8Block];
+  __shared__ float ss0[2][BM], ss1[2][BM];  // row scale * scale of either block of 128 weight rows
+
+  const int nbx = (a.N + kBN - 1) / kBN;
+  PlanItem tile;
+  int bx;
+  if (!my_work(a, BM, nbx, tile, bx)) return;
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave_id = __builtin_amdgcn_readfirstlane(tid / kWave), wave = wave_id % kNW;
+  const int lr = lane & 15, lg = lane >> 4;
+  const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
+  const int col0 = bx * kBN + wave * kNT * 16, m0 = wave_id / kNW * RB * 16;
+  const int nbr = (a.N + kFp8Block - 1) / kFp8Block;
+  // pass p of either operand: row 64 p + tid / 8, the piece that belongs at place tid % 8
+  const int piece = piece_of_lane(lane);
+  const uint8_t *ap[PASS];
+  uint32_t wo[PASS];  // rows of the tile's columns, from the first one's weights
+  const uint8_t *wbase = a.w0 + (int64_t(tile.expert) * a.N + bx * kBN) * K;
+#pragma unroll
+  for (int p = 0; p < PASS; ++p) {
+    const int m = p * (kHugeThreads / kPieces) + tid / kPieces;
+    const int r = m < tile.rows ? source_row(a, tile.row0 + m) : -1;
+    ap[p] = static_cast<const uint8_t *>(a.a) + int64_t(max(r, 0)) * K;
+    wo[p] = uint32_t(min(m, a.N - 1 - bx * kBN)) * uint32_t(K);
+  }
+  const int sm = tid % BM, sn = tid / BM;
+  const int srow = sm < tile.rows ? source_row(a, tile.row0 + sm) : -1;
+  const float *sap = a.as + max(srow, 0);
+  const float *swp = a.s0 + (int64_t(tile.expert) * nbr + min(bx * (kBN / kFp8Block) + sn, nbr - 1)) * nb;
+
+  float sga, sgw;
+  auto load = [&](int s, uint8_t *ba, uint8_t *bw) {
+    s = min(s, nb - 1);
+    const int k = min(s * kFp8Block + piece * 16, K - 16);
+#pragma unroll
+    for (int p = 0; p < PASS; ++p) {
+      const int at = (p * (kHugeThreads / kWave) + wave_id) * (kWave * 16);
+      to_lds(ap[p] + k, ba + at);
+      to_lds(wbase + (wo[p] + uint32_t(k)), bw + at);
     }
     sga = sap[int64_t(s) * a.a_rows];
     sgw = swp[s];
@@ -441,55 +599,62 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
   for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
     for (int mt = 0; mt < RB; ++mt) acc[nt][mt] = fp8_acc{0.f, 0.f, 0.f, 0.f};
-  const uint32_t x0 = uint32_t(lr) * kFp8Block + ((lg ^ (lr & 7)) * 16);
-  const uint32_t x1 = uint32_t(lr) * kFp8Block + (((lg + 4) ^ (lr & 7)) * 16);
-  // one block; TAIL: it reaches past the end of the reduction, where the
+  const uint32_t r0 = piece_at(lr, lg), r1 = piece_at(lr, lg + 4);
+  // one block; TAIL: it may reach past the end of the reduction, where the
   // codes count as zero in both operands (a stray one may be a NaN)
-  auto block = [&](int s, const uint8_t *buf, const float (&ss)[2][BM], const uint4 (&w)[kNT][2], auto tail) {
+  auto block = [&](int s, const uint8_t *ba, const uint8_t *bw, const float (&ss)[2][BM], auto tail) {
     constexpr bool TAIL = decltype(tail)::value;
     const bool ok0 = s * kFp8Block + lg * 16 < K, ok1 = s * kFp8Block + 64 + lg * 16 < K;
-    auto codes = [&](const uint4 &lo, const uint4 &hi) {
+    auto read = [&](const uint8_t *b, int row) {
+      const uint4 lo = *reinterpret_cast<const uint4 *>(b + row * kFp8Block + r0);
+      const uint4 hi = *reinterpret_cast<const uint4 *>(b + row * kFp8Block + r1);
       return Fp8Operand<false>(TAIL ? join8(keep(lo, ok0), keep(hi, ok1)) : join8(lo, hi));
     };
+    const Fp8Operand<false> w[kNT] = {read(bw, wave * 64), read(bw, wave * 64 + 16), read(bw, wave * 64 + 32),
+                                      read(bw, wave * 64 + 48)};
+    Fp8Operand<false> x = read(ba, m0);
+    float sc = ss[wave / 2][m0 + lr];
 #pragma unroll
     for (int mt = 0; mt < RB; ++mt) {
-      const Fp8Operand<false> x = codes(*reinterpret_cast<const uint4 *>(buf + x0 + mt * 16 * kFp8Block),
-                                        *reinterpret_cast<const uint4 *>(buf + x1 + mt * 16 * kFp8Block));
-      const float sc = ss[wave / 2][mt * 16 + lr];
+      const Fp8Operand<false> xn = read(ba, m0 + min(mt + 1, RB - 1) * 16);  // read while this one multiplies
+      const float scn = ss[wave / 2][m0 + min(mt + 1, RB - 1) * 16 + lr];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        const fp8_acc d = fp8_product(codes(w[nt][0], w[nt][1]), x);
+        const fp8_acc d = fp8_product(w[nt], x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nt][mt][i] = __builtin_fmaf(d[i], sc, acc[nt][mt][i]);
       }
+      x = xn, sc = scn;
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   const int whole = K / kFp8Block;  // blocks without a tail
-  load(0, sa0, w0);
+  load(0, sa0, sw0);
   stage_scale(ss0);
   __syncthreads();
   int s = 0;
   for (; s + 1 < whole; s += 2) {
-    load(s + 1, sa1, w1);
-    block(s, sa0, ss0, w0, std::false_type{});
+    load(s + 1, sa1, sw1);
+    block(s, sa0, sw0, ss0, std::false_type{});
     stage_scale(ss1);
     __syncthreads();
-    load(s + 2, sa0, w0);
-    block(s + 1, sa1, ss1, w1, std::false_type{});
+    load(s + 2, sa0, sw0);
+    block(s + 1, sa1, sw1, ss1, std::false_type{});
     stage_scale(ss0);
     __syncthreads();
   }
   // at most two blocks are left, the last perhaps short
   if (s < nb) {
-    load(s + 1, sa1, w1);
-    block(s, sa0, ss0, w0, std::true_type{});
+    load(s + 1, sa1, sw1);
+    block(s, sa0, sw0, ss0, std::true_type{});
     stage_scale(ss1);
     __syncthreads();
-    if (s + 1 < nb) block(s + 1, sa1, ss1, w1, std::true_type{});
+    if (s + 1 < nb) block(s + 1, sa1, sw1, ss1, std::true_type{});
   }
 #pragma unroll
   for (int mt = 0; mt < RB; ++mt) {
-    const int m = mt * 16 + lr;
+    const int m = m0 + mt * 16 + lr;
     if (m < tile.rows) {
       const bool ok = source_row(a, tile.row0 + m) >= 0;
       const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
@@ -509,14 +674,15 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
   constexpr int NTH = MODE == kGated ? WN / 2 : WN;
   constexpr int COLS = (kNW / KW) * NTH * 16;
   constexpr int XB = SRC == kSrcCodes ? 1 : SRC == kDtF32 ? 4 : 2;  // bytes per activation
-  constexpr int DEPTH = WN >= 4 || XB == 4 ? 2 : 4;                  // blocks in flight per wave
+  constexpr int DEPTH = XB == 4 ? 3 : 4;  // blocks in flight per wave
+  __shared__ __align__(16) uint8_t turn[kNW][WN][kTileBytes];
   __shared__ float part[KW > 1 ? kNW : 1][KW > 1 ? WN * 4 : 1][kWave];
 
   const int nbx = (a.N + COLS - 1) / COLS;
   PlanItem tile;
   int bx;
   if (!my_work(a, 16, nbx, tile, bx)) return;
-  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
   const int lr = lane & 15, lg = lane >> 4;
   const int kz = wave % KW;
   const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
@@ -532,22 +698,23 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
     const bool up = MODE == kGated && nt >= NTH;
     const int row = min(col0 + (nt % NTH) * 16, a.N - 16) + (up && a.fused ? a.N : 0);
     const bool second = up && !a.fused;
-    wp[nt] = (second ? a.w1 : a.w0) + (int64_t(tile.expert) * n_rows + row + lr) * K + lg * 16;
+    wp[nt] = (second ? a.w1 : a.w0) + (int64_t(tile.expert) * n_rows + row) * K;
     sp[nt] = (second ? a.s1 : a.s0) + (int64_t(tile.expert) * nbr + row / kFp8Block) * nb;
   }
   const int r = lr < tile.rows ? source_row(a, tile.row0 + lr) : -1;
   const bool rok = r >= 0;
+  // (rows past the tile read row 0, which the others of their kind share)
   const char *xp = static_cast<const char *>(a.a) + int64_t(max(r, 0)) * K * XB;
   const float *sxp = SRC == kSrcCodes ? a.as + max(r, 0) : nullptr;
 
-  uint4 wq[DEPTH][WN][2], xq[DEPTH][2][XB];
+  WeightTile wq[DEPTH][WN];
+  uint4 xq[DEPTH][2][XB];
   float sq[DEPTH][WN], sx[DEPTH];
   auto load = [&](int s, int d) {
     const int k0 = s * kFp8Block;
 #pragma unroll
     for (int nt = 0; nt < WN; ++nt) {
-      wq[d][nt][0] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0, K - 16 - lg * 16));
-      wq[d][nt][1] = *reinterpret_cast<const uint4 *>(wp[nt] + min(k0 + 64, K - 16 - lg * 16));
+      wq[d][nt].load(wp[nt], K, k0);
       sq[d][nt] = sp[nt][s];
     }
 #pragma unroll
@@ -595,11 +762,12 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
       }
     }
     const Fp8Operand<true> xo(x);
+#pragma unroll
+    for (int nt = 0; nt < WN; ++nt) wq[d][nt].put(turn[wave][nt], K, k0);
     const float sxv = rok ? sx[d] : 0.f;
 #pragma unroll
     for (int nt = 0; nt < WN; ++nt) {
-      const fp8_acc v =
-          fp8_product(Fp8Operand<true>(join8(keep(wq[d][nt][0], ok[0]), keep(wq[d][nt][1], ok[1]))), xo);
+      const fp8_acc v = fp8_product(Fp8Operand<true>(tile_operand(turn[wave][nt])), xo);
       const float sc = sxv * sq[d][nt];
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[nt][i] = __builtin_fmaf(v[i], sc, acc[nt][i]);
@@ -671,6 +839,11 @@ void launch_wide(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   launch(fp8_wide_kernel, dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
 }
 
+void launch_huge(const Fp8Args &a, int64_t tiles, hipStream_t s) {
+  const int64_t nbx = (a.N + kBN - 1) / kBN;
+  launch(fp8_huge_kernel, dim3(unsigned(tiles * nbx)), dim3(kHugeThreads), 0, s, a);
+}
+
 template <int KW, int WN, int MODE, int SRC>
 void launch_decode_one(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   constexpr int COLS = (kNW / KW) * (MODE == kGated ? WN / 2 : WN) * 16;
@@ -717,7 +890,7 @@ int64_t fp8_ffn_groups(const moe_layer_desc *d, int32_t T) {
 // Rows per tile, by the mean rows of an expert: 16 (the decode kernel), 64,
 // or 128 where the 8-bit instruction is used.
 int fp8_tile_rows(int64_t rows, int experts, bool exact) {
-  return rows <= 16LL * experts ? 16 : exact || rows <= 96LL * experts ? 64 : 128;
+  return rows <= 16LL * experts ? 16 : exact || rows <= 96LL * experts ? 64 : rows <= 1024LL * experts ? 128 : 256;
 }
 
 void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_t a_rows, const uint8_t *a,
@@ -736,7 +909,8 @@ void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, in
   if (bm == 16) launch_decode<kPlain, kSrcCodes>(g, tiles, s);
   else if (exact) launch_tile<kPlain, true>(g, tiles, s);
   else if (bm == 64) launch_tile<kPlain, false>(g, tiles, s);
-  else launch_wide(g, tiles, s);
+  else if (bm == 128) launch_wide(g, tiles, s);
+  else launch_huge(g, tiles, s);
 }
 
 // Workspace of the expert FFN: x codes and scales (tile kernels), h as codes

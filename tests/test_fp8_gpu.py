@@ -157,6 +157,10 @@ PRODUCT = [
     (257, 256, 128, 1, None, True, "bf16"),
     (515, 16, 2064, 2, "one", False, "f32"),
     (600, 1040, 256, 4, "random", True, "bf16"),
+    (1300, 528, 272, 1, None, False, "bf16"),        # 256-row tiles: row, column and reduction tails
+    (1100, 256, 400, 1, None, True, "f16"),
+    (1200, 144, 256, 1, None, True, "f32"),
+    (2300, 64, 144, 2, "tail", True, "bf16"),
     (37, 64, 4096, 600, "random", False, "f32"),     # more experts than rows, long reduction
 ]
 
@@ -208,32 +212,34 @@ def test_product(rows, N, K, E, kind, gathered, out):
     assert torch.equal(y.view(torch.uint8), run_product(case, rows, N, K, E, out).view(torch.uint8))
 
 
-@pytest.mark.parametrize("rows", [20, 200, 700])
-def test_product_bad_tables(rows):
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [20, 200, 700, 4500])
+def test_product_bad_tables(rows, out):
     """A map entry outside the rows gives zeros; wild offsets stay inside the output."""
     N, K, E = 64, 272, 4
     case = list(product_case(rows, N, K, E, "random", True, rows))
     row_map = case[5]
     bad = torch.arange(0, rows, 7)
     row_map[bad] = torch.tensor([-1, 1 << 30, case[0].shape[0]], dtype=torch.int32).repeat(rows)[:len(bad)]
-    y = run_product(case, rows, N, K, E, "f32")
+    y = run_product(case, rows, N, K, E, out)
     assert (y[bad] == 0).all()
     case[4] = torch.tensor([-5, 3, rows + 9, 1 << 30, -7], dtype=torch.int32)
-    y = run_product(case, rows, N, K, E, "f32")  # ranges [0, 3), [3, rows), [rows, rows), [rows, rows)
+    y = run_product(case, rows, N, K, E, out)  # ranges [0, 3), [3, rows), [rows, rows), [rows, rows)
     case[4] = torch.tensor([0, 3, rows, rows, rows], dtype=torch.int32)
-    assert torch.equal(y, run_product(case, rows, N, K, E, "f32"))
+    assert torch.equal(y, run_product(case, rows, N, K, E, out))
 
 
-@pytest.mark.parametrize("rows,E", [(6, 1), (150, 2), (300, 2)])
-def test_product_padding_is_not_read(rows, E):
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,E", [(6, 1), (150, 2), (300, 2), (1100, 1)])
+def test_product_padding_is_not_read(rows, E, out):
     """NaN codes outside a row's reduction (the next row's, a neighbour expert's) do not reach it."""
     N, K = 48, 144  # 16 codes past one block
     case = product_case(rows, N, K, E, "random" if E > 1 else None, False, 5)
     a, w = case[0], case[2]
-    y0 = run_product(case, rows, N, K, E, "f32")
+    y0 = run_product(case, rows, N, K, E, out)
     w[:, 7, :] = 0x7F
     a[rows // 2, :] = 0x7F
-    y1 = run_product(case, rows, N, K, E, "f32")
+    y1 = run_product(case, rows, N, K, E, out)
     keep_n = torch.arange(N) != 7
     keep_r = torch.arange(rows) != rows // 2
     assert torch.equal(y1[keep_r][:, keep_n], y0[keep_r][:, keep_n])
