@@ -869,8 +869,26 @@ void launch_decode(const Fp8Args &a, int64_t tiles, hipStream_t s) {
 
 }  // namespace
 
+// Rows per tile: 16 (the decode kernel), 64, or for the 8-bit instruction 128
+// or 256.  Measured for K = 2048 and bf16 results, us with 16 / 64 / 128
+// rows (256 where given): one matrix of N = 4096, 128 rows 10.8 / 23.6 / 33,
+// 256 rows 18 / 24 / 34, 512 rows 32 / 24.5 / 35, 2048 rows 113 / 37 / 38,
+// 4096 rows 211 / 66 / 51, 8192 rows - / 125 / 97 / 93; 64 matrices of
+// N = 1024 with 16 rows each 25 / 26 / 35, 32 rows 38 / 27 / 36, 128 rows
+// 135 / 38 / 41, 256 rows 250 / 73 / 51.  So: 16 while its workgroups fill
+// the GPU at most about once over, or at most 16 rows an expert; 64 while its
+// workgroups fit the GPU at once, or experts would leave a larger tile half
+// empty; 256 from two of its tiles per CU on.
+int fp8_tile_rows(int64_t rows, int32_t N, int32_t K, int experts, bool exact) {
+  const int64_t t16 = most_tiles(rows, experts, 16), t64 = most_tiles(rows, experts, 64);
+  const int dc = decode_cols(K, false), nbx = (N + kBN - 1) / kBN;
+  if (rows <= 16LL * experts || t16 * ((N + dc - 1) / dc) <= 2560) return 16;
+  if (exact || rows < 96LL * experts || t64 * nbx <= 640) return 64;
+  return rows / kHugeRows * nbx >= 512 && rows >= 1024LL * experts ? 256 : 128;
+}
+
 int64_t fp8_matmul_groups(int64_t rows, int32_t N, int32_t K, int32_t n_experts, bool offsets, bool exact) {
-  const int bm = fp8_tile_rows(rows, n_experts, exact);
+  const int bm = fp8_tile_rows(rows, N, K, n_experts, exact);
   const int64_t tiles = offsets ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
   const int cols = bm == 16 ? decode_cols(K, false) : kBN;
   return tiles * ((N + cols - 1) / cols);
@@ -887,12 +905,6 @@ int64_t fp8_ffn_groups(const moe_layer_desc *d, int32_t T) {
   return ffn_tiles(d, T) * std::max((d->d_ff + gc - 1) / gc, (d->d_model + dc - 1) / dc);
 }
 
-// Rows per tile, by the mean rows of an expert: 16 (the decode kernel), 64,
-// or 128 where the 8-bit instruction is used.
-int fp8_tile_rows(int64_t rows, int experts, bool exact) {
-  return rows <= 16LL * experts ? 16 : exact || rows <= 96LL * experts ? 64 : rows <= 1024LL * experts ? 128 : 256;
-}
-
 void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_t a_rows, const uint8_t *a,
                        const float *a_scales, const int32_t *row_map, const int32_t *expert_off, const uint8_t *w,
                        const float *w_scales, void *y, int32_t out_dtype, void *stream) {
@@ -904,7 +916,7 @@ void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, in
   g.E = n_experts, g.expert_off = expert_off;
   g.out = y, g.out_dtype = out_dtype;
   const bool exact = out_dtype == MOE_DT_F32;
-  const int bm = fp8_tile_rows(rows, n_experts, exact);
+  const int bm = fp8_tile_rows(rows, N, K, n_experts, exact);
   const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
   if (bm == 16) launch_decode<kPlain, kSrcCodes>(g, tiles, s);
   else if (exact) launch_tile<kPlain, true>(g, tiles, s);
