@@ -20,7 +20,8 @@
 // cut into three bf16 pieces of 8 significant bits each (24 in all, so
 // nothing is lost), fp16 values into two, and the products of pieces above
 // 2^-24 of the largest are added: 3 products for bf16 layers, 5 for fp16 and
-// 6 for fp32, each at 16 times the fp32 matrix rate.
+// 6 for fp32, each at 16 times the fp32 matrix rate.  dl is cut once, where
+// it is made, and kept as three planes.
 //
 // Softmax, sums over tokens and the loss are per-wave rows and two-level sums
 // in a fixed order: no floating-point atomics.
@@ -39,6 +40,8 @@ constexpr int kTile = 64;             // output rows and columns per workgroup
 constexpr int kStep = 64;             // reduction elements per LDS stage
 constexpr int kLds = kStep + 8;       // 16-bit elements per LDS row: 16 rows' 16-byte pieces on different banks
 constexpr int kChunkTokens = 4;       // tokens per wave of the row kernels
+constexpr int kPieces = 3;            // bf16 pieces of an fp32 value
+constexpr int kDtPieces = 3;          // operand type: three bf16 planes (beside the moe_dtype values)
 
 // ---- the split products -----------------------------------------------------
 
@@ -48,6 +51,7 @@ struct Operand {
   int64_t ld;
   int rows;
   int vec;  // rows start 16-byte aligned: whole pieces load as vectors
+  int64_t plane = 0;  // kDtPieces: elements per plane; ld is a multiple of 8, zero past the end of a row
 };
 // Tokens that take part (the reduction of dW runs over tokens): null mask and
 // off for all of them.
@@ -75,7 +79,7 @@ struct GemmArgs {
 
 template <int DT>
 constexpr int pieces(bool native) {
-  return DT == kDtBF16 || native ? 1 : DT == kDtF16 ? 2 : 3;
+  return DT == kDtBF16 || native ? 1 : DT == kDtF16 ? 2 : kPieces;
 }
 
 // v as bf16 pieces: cut (not rounded) to 8 significant bits, the rest cut
@@ -100,160 +104,272 @@ __device__ __forceinline__ void split(float v, uint32_t (&out)[P]) {
   }
 }
 
-// Staging of a 64 x 64 tile of one operand.  KC: a thread takes 16
-// consecutive reduction elements of one row; else 4 x 4 elements, turned
-// around in registers, so that LDS always holds [row][k].
-template <int DT, bool KC, bool NATIVE>
+// Staging of 64 rows by 64 reduction elements of one operand.  KC: a thread
+// takes 16 consecutive reduction elements of one row; else 4 x 4 elements
+// (4 neighbouring rows at 4 reduction elements), turned around in registers,
+// so that LDS always holds [row][k].  Loads go to clamped addresses without
+// a condition and their values are touched only in store(), so that they
+// stay in flight in between.  Reduction elements that do not exist (or do not
+// take part) are zeroed there; rows that do not exist are not: they reach
+// only results that are not stored.
+// VEC: rows are 16-byte aligned (16-bit KC and fp32: whole 16-byte pieces;
+// 16-bit rows side by side: 8-byte ones).
+template <int DT, bool KC, bool NATIVE, bool VEC>
 struct Stage {
   static constexpr int P = pieces<DT>(NATIVE);
-  float v[16];
-  static __device__ __forceinline__ float elt(const Operand &o, int64_t i) { return load_act<DT>(o.p, i); }
-  // n elements from i (vector loads where aligned and whole), zero past `have`.
-  template <int N>
-  static __device__ __forceinline__ void run(const Operand &o, int64_t i, int have, float *dst) {
-    if (o.vec && have >= N) {
-      if constexpr (DT == kDtF32) {
-#pragma unroll
-        for (int u = 0; u < N / 4; ++u) {
-          const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(o.p) + i + 4 * u);
-          dst[4 * u] = f.x, dst[4 * u + 1] = f.y, dst[4 * u + 2] = f.z, dst[4 * u + 3] = f.w;
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < N / 4; ++u) {
-          const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(o.p) + i + 4 * u);
-          dst[4 * u] = half_lo<DT>(w.x), dst[4 * u + 1] = half_hi<DT>(w.x);
-          dst[4 * u + 2] = half_lo<DT>(w.y), dst[4 * u + 3] = half_hi<DT>(w.y);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < N; ++u) dst[u] = u < have ? elt(o, i + u) : 0.f;
-    }
-  }
+  static constexpr bool RAW = P == 1;  // 16-bit elements that are copied as they are
+  static constexpr int W = DT == kDtF32 || !VEC ? 16 : 8;  // words: one or two elements each
+  uint32_t w[W];
+  uint32_t on;  // bit j: reduction element j of the four takes part
   template <bool MASK>
   __device__ __forceinline__ void load(const Operand &o, int row0, int k0, int K, const Tokens &tk, int lo, int hi) {
     const int tid = threadIdx.x;
+    const float *pf = static_cast<const float *>(o.p);
+    const uint16_t *ph = static_cast<const uint16_t *>(o.p);
     if constexpr (KC) {
-      const int r = row0 + tid / 4, k = k0 + tid % 4 * 16;
-      run<16>(o, int64_t(min(r, o.rows - 1)) * o.ld + k, r < o.rows ? K - k : 0, v);
+      const int64_t row = int64_t(min(row0 + tid / 4, o.rows - 1)) * o.ld;
+      const int k = k0 + tid % 4 * 16;
+      if constexpr (!VEC) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = word(pf, ph, row + min(k + u, K - 1));
+      } else {
+        constexpr int C = DT == kDtF32 ? 4 : 8;  // elements of a 16-byte piece
+#pragma unroll
+        for (int u = 0; u < 16 / C; ++u) {
+          const int64_t at = row + min(k + C * u, K - C);
+          const uint4 q = DT == kDtF32 ? *reinterpret_cast<const uint4 *>(pf + at)
+                                       : *reinterpret_cast<const uint4 *>(ph + at);
+          w[4 * u] = q.x, w[4 * u + 1] = q.y, w[4 * u + 2] = q.z, w[4 * u + 3] = q.w;
+        }
+      }
     } else {
       const int k = k0 + tid / 16 * 4, r = row0 + tid % 16 * 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        bool ok = k + j < K;
-        if constexpr (MASK) ok = ok && k + j >= lo && k + j < hi && (!tk.mask || tk.mask[k + j]);
-        run<4>(o, int64_t(ok ? k + j : 0) * o.ld + r, ok ? o.rows - r : 0, &v[4 * j]);
+        const int64_t at = int64_t(min(k + j, K - 1)) * o.ld;
+        if constexpr (!VEC) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) w[4 * j + u] = word(pf, ph, at + min(r + u, o.rows - 1));
+        } else if constexpr (DT == kDtF32) {
+          const uint4 q = *reinterpret_cast<const uint4 *>(pf + at + min(r, o.rows - 4));
+          w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2 *>(ph + at + min(r, o.rows - 4));
+          w[2 * j] = q.x, w[2 * j + 1] = q.y;
+        }
+      }
+      on = 15;
+      if constexpr (MASK) {
+        if (tk.mask) {
+          on = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) on |= uint32_t(tk.mask[min(k + j, K - 1)] != 0) << j;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k + j < lo || k + j >= hi) on &= ~(1u << j);
       }
     }
   }
-  __device__ __forceinline__ uint32_t bits(float f, uint32_t (&q)[P]) {
-    if constexpr (NATIVE) q[0] = f32_to_f16_bits(f);
-    else split<P>(f, q);
-    return q[0];
+  static __device__ __forceinline__ uint32_t word(const float *pf, const uint16_t *ph, int64_t i) {
+    if constexpr (DT == kDtF32) return __float_as_uint(pf[i]);
+    else return ph[i];
   }
-  __device__ __forceinline__ void store(uint16_t (&lds)[P][kTile][kLds]) {
+  // Element u of the 16: its 16 bits (16-bit types) or its value.
+  __device__ __forceinline__ uint32_t half_bits(int u) const {
+    if constexpr (W == 16) return w[u];
+    else return u & 1 ? w[u / 2] >> 16 : w[u / 2] & 0xffffu;
+  }
+  __device__ __forceinline__ void cut(int u, bool ok, uint32_t (&q)[P]) const {
+    if constexpr (RAW) q[0] = ok ? half_bits(u) : 0u;
+    else if constexpr (DT == kDtF32) split<P>(ok ? __uint_as_float(w[u]) : 0.f, q);
+    else split<P>(ok ? half_to_f32<DT>(half_bits(u)) : 0.f, q);
+  }
+  // into LDS rows row0 .. row0 + 63; k0, K as loaded
+  template <int ROWS>
+  __device__ __forceinline__ void store(uint16_t (&lds)[P][ROWS][kLds], int row0, int k0, int K) const {
     const int tid = threadIdx.x;
     if constexpr (KC) {
-      uint32_t w[P][8];
+      const int k = k0 + tid % 4 * 16;
+      uint32_t o[P][8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        uint32_t x[P], y[P];
-        bits(v[2 * u], x), bits(v[2 * u + 1], y);
+        if constexpr (RAW && W == 8) {
+          o[0][u] = k + (u / 4) * 8 < K ? w[u] : 0u;  // K is a multiple of 8
+        } else {
+          uint32_t x[P], y[P];
+          cut(2 * u, k + 2 * u < K, x), cut(2 * u + 1, k + 2 * u + 1 < K, y);
 #pragma unroll
-        for (int p = 0; p < P; ++p) w[p][u] = x[p] | (y[p] << 16);
+          for (int p = 0; p < P; ++p) o[p][u] = x[p] | (y[p] << 16);
+        }
       }
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        uint4 *q = reinterpret_cast<uint4 *>(&lds[p][tid / 4][tid % 4 * 16]);
-        q[0] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
-        q[1] = make_uint4(w[p][4], w[p][5], w[p][6], w[p][7]);
+        uint4 *q = reinterpret_cast<uint4 *>(&lds[p][row0 + tid / 4][tid % 4 * 16]);
+        q[0] = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+        q[1] = make_uint4(o[p][4], o[p][5], o[p][6], o[p][7]);
       }
     } else {
+      const int k = k0 + tid / 16 * 4;
+      bool ok[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // row i of the 4 x 4 elements
+      for (int j = 0; j < 4; ++j) ok[j] = k + j < K && ((on >> j) & 1u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // row i of the four
         uint32_t x[4][P];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bits(v[4 * j + i], x[j]);
+        for (int j = 0; j < 4; ++j) cut(4 * j + i, ok[j], x[j]);
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          *reinterpret_cast<uint2 *>(&lds[p][tid % 16 * 4 + i][tid / 16 * 4]) =
+          *reinterpret_cast<uint2 *>(&lds[p][row0 + tid % 16 * 4 + i][tid / 16 * 4]) =
               make_uint2(x[0][p] | (x[1][p] << 16), x[2][p] | (x[3][p] << 16));
       }
     }
   }
 };
 
-// C[m][n] = sum_k A(m, k) B(n, k) over one part of the reduction.  A wave
-// makes 32 x 32 outputs (operand a of the matrix cores: columns n, so that a
-// lane's four results are neighbours in a row of C).  NATIVE: fp16 operands
+// The same of values that lie cut into three planes already: copied as they are.
+template <bool KC>
+struct Stage<kDtPieces, KC, false, true> {
+  static constexpr int P = kPieces;
+  uint32_t w[P][8];  // (words: arrays of vectors here went to scratch memory)
+  template <bool MASK>
+  __device__ __forceinline__ void load(const Operand &o, int row0, int k0, int K, const Tokens &, int, int) {
+    const int tid = threadIdx.x;
+    const uint16_t *base = static_cast<const uint16_t *>(o.p);
+    if constexpr (KC) {  // 16 elements of a row
+      const int64_t row = int64_t(min(row0 + tid / 4, o.rows - 1)) * o.ld;
+      const int k = k0 + tid % 4 * 16;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q = *reinterpret_cast<const uint4 *>(base + p * o.plane + row + min(k + 8 * h, int(o.ld) - 8));
+          w[p][4 * h] = q.x, w[p][4 * h + 1] = q.y, w[p][4 * h + 2] = q.z, w[p][4 * h + 3] = q.w;
+        }
+    } else {  // 4 x 4 elements, two words for each reduction element
+      const int k = k0 + tid / 16 * 4, r = min(row0 + tid % 16 * 4, int(o.ld) - 4);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint2 q =
+              *reinterpret_cast<const uint2 *>(base + p * o.plane + int64_t(min(k + j, K - 1)) * o.ld + r);
+          w[p][2 * j] = q.x, w[p][2 * j + 1] = q.y;
+        }
+    }
+  }
+  template <int ROWS>
+  __device__ __forceinline__ void store(uint16_t (&lds)[P][ROWS][kLds], int row0, int k0, int K) const {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if constexpr (KC) {  // (elements past K, up to a multiple of 8, are zero in memory)
+        const int k = k0 + tid % 4 * 16;
+        uint4 *q = reinterpret_cast<uint4 *>(&lds[p][row0 + tid / 4][tid % 4 * 16]);
+        const bool a = k < K, b = k + 8 < K;
+        q[0] = make_uint4(a ? w[p][0] : 0u, a ? w[p][1] : 0u, a ? w[p][2] : 0u, a ? w[p][3] : 0u);
+        q[1] = make_uint4(b ? w[p][4] : 0u, b ? w[p][5] : 0u, b ? w[p][6] : 0u, b ? w[p][7] : 0u);
+      } else {
+        const int k = k0 + tid / 16 * 4;
+        uint32_t v[8];  // [reduction element][pair of rows]
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = k + j / 2 < K ? w[p][j] : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;  // high or low halves of two words
+          *reinterpret_cast<uint2 *>(&lds[p][row0 + tid % 16 * 4 + i][tid / 16 * 4]) =
+              make_uint2(__builtin_amdgcn_perm(v[2 + (i >> 1)], v[i >> 1], sel),
+                         __builtin_amdgcn_perm(v[6 + (i >> 1)], v[4 + (i >> 1)], sel));
+        }
+      }
+    }
+  }
+};
+
+// C[m][n] = sum_k A(m, k) B(n, k) over one part of the reduction, tiles of
+// 64 x 64.  A wave makes 32 x 32 outputs (operand a of the matrix cores:
+// columns n, so that a lane's four results are neighbours in a row of C).  Two steps are in flight in registers while one is multiplied: a step's
+// products take a fraction of a memory round trip.  NATIVE: fp16 operands
 // multiplied as they are.  MASK: reduction elements outside `tokens` count as
 // zeros, whatever they hold.
-template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK>
+template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK, bool VECB>
 __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
-  using SA = Stage<DTA, KCA, NATIVE>;
-  using SB = Stage<DTB, KCB, NATIVE>;
-  constexpr int PA = SA::P, PB = SB::P;
-  __shared__ __align__(16) uint16_t la[PA][kTile][kLds], lb[PB][kTile][kLds];
+  using SA = Stage<DTA, KCA, NATIVE, true>;
+  using SB = Stage<DTB, KCB, NATIVE, VECB>;
+  constexpr int PA = SA::P, PB = SB::P, S = 2, TILE = kTile;
+  __shared__ __align__(16) uint16_t la[PA][TILE][kLds], lb[PB][TILE][kLds];
   const int lane = lane_id(), wave = threadIdx.x / kWave, lr = lane & 15, lg = lane >> 4;
-  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+  const int m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE;
+  const int wm = (wave >> 1) * 16 * S, wn = (wave & 1) * 16 * S;
   const int s0 = int(blockIdx.z) * g.per, s1 = min(s0 + g.per, (g.K + kStep - 1) / kStep);
   int lo = 0, hi = 0;
   if constexpr (MASK) token_range(g.tokens, lo, hi);
-  f32x4 acc[2][2];
+  f32x4 acc[S][S];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  SA sa;
-  SB sb;
-  auto load = [&](int s) {
-    sa.template load<MASK>(g.a, m0, s * kStep, g.K, g.tokens, lo, hi);
-    sb.template load<MASK>(g.b, n0, s * kStep, g.K, g.tokens, lo, hi);
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  SA sa[2];
+  SB sb[2];
+  auto load = [&](int s, auto rc) {
+    constexpr int r = decltype(rc)::value;
+    sa[r].template load<MASK>(g.a, m0, s * kStep, g.K, g.tokens, lo, hi);
+    sb[r].template load<MASK>(g.b, n0, s * kStep, g.K, g.tokens, lo, hi);
   };
-  if (s0 < s1) load(s0);
-  for (int s = s0; s < s1; ++s) {
+  auto step = [&](int s, auto rc) {
+    constexpr int r = decltype(rc)::value;
     __syncthreads();
-    sa.store(la);
-    sb.store(lb);
+    sa[r].store(la, 0, s * kStep, g.K);
+    sb[r].store(lb, 0, s * kStep, g.K);
     __syncthreads();
-    if (s + 1 < s1) load(s + 1);
+    if (s + 2 < s1) load(s + 2, rc);
 #pragma unroll
     for (int kk = 0; kk < kStep; kk += 32) {
-      uint4 fa[PA][2], fb[PB][2];
+      uint4 fa[PA][S];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int p = 0; p < PA; ++p)
 #pragma unroll
-        for (int p = 0; p < PA; ++p)
+        for (int i = 0; i < S; ++i)
           fa[p][i] = *reinterpret_cast<const uint4 *>(&la[p][wm + i * 16 + lr][kk + lg * 8]);
 #pragma unroll
-        for (int p = 0; p < PB; ++p)
-          fb[p][i] = *reinterpret_cast<const uint4 *>(&lb[p][wn + i * 16 + lr][kk + lg * 8]);
-      }
+      for (int q = PB - 1; q >= 0; --q)
 #pragma unroll
-      for (int p = PA - 1; p >= 0; --p)
+        for (int j = 0; j < S; ++j) {
+          const uint4 fb = *reinterpret_cast<const uint4 *>(&lb[q][wn + j * 16 + lr][kk + lg * 8]);
 #pragma unroll
-        for (int q = PB - 1; q >= 0; --q)
-          if (p + q <= 2)
+          for (int p = PA - 1; p >= 0; --p)
+            if (p + q < kPieces)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int i = 0; i < S; ++i) {
                 if constexpr (NATIVE)
-                  acc[i][j] = mfma_f16(__builtin_bit_cast(f16x8, fb[q][j]), __builtin_bit_cast(f16x8, fa[p][i]),
-                                       acc[i][j]);
+                  acc[i][j] = mfma_f16(__builtin_bit_cast(f16x8, fb), __builtin_bit_cast(f16x8, fa[p][i]), acc[i][j]);
                 else
-                  acc[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, fb[q][j]), __builtin_bit_cast(bf16x8, fa[p][i]),
-                                        acc[i][j]);
+                  acc[i][j] =
+                      mfma_bf16(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, fa[p][i]), acc[i][j]);
               }
+        }
     }
+  };
+  using R0 = std::integral_constant<int, 0>;
+  using R1 = std::integral_constant<int, 1>;
+  if (s0 < s1) {
+    load(s0, R0{});
+    load(min(s0 + 1, s1 - 1), R1{});
+    int s = s0;
+    for (; s + 1 < s1; s += 2) {
+      step(s, R0{});
+      step(s + 1, R1{});
+    }
+    if (s < s1) step(s, R0{});
   }
   float *out = g.out + int64_t(blockIdx.z) * g.part;
   const int N = g.b.rows;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < S; ++i) {
     const int m = m0 + wm + i * 16 + lr;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < S; ++j) {
       const int n = n0 + wn + j * 16 + 4 * lg;
       if (m >= g.a.rows || n >= N) continue;
       float v[4];
@@ -303,7 +419,7 @@ struct RowArgs {
   const float *dloss;
   const float *dtopk;      // [T][K] or null
   int renorm;
-  float *dl;               // [T][ld]
+  uint16_t *dl;            // bf16 pieces [3][T][ld], zero past E
   int ld;
   float *dbias;            // [chunks][E] partial sums, or null
 };
@@ -312,22 +428,21 @@ struct RowArgs {
 template <int EPL>
 __device__ __forceinline__ void load_row(const RowArgs &a, int t, float (&l)[EPL]) {
   const int lane = lane_id();
-  const int64_t at = int64_t(t) * a.E;
+  const int64_t at = int64_t(t) * a.E, part = int64_t(a.tokens.T) * a.E;
+  const float *src = a.parts ? a.parts : a.logits;
+  const int nz = a.parts ? a.z : 1;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + kWave * i;
-    l[i] = -INFINITY;
-    if (e < a.E) {
-      if (a.parts) {
-        float s = 0.f;
-        for (int z = 0; z < a.z; ++z) s += a.parts[int64_t(z) * a.tokens.T * a.E + at + e];
-        l[i] = s + (a.bias ? a.bias[e] : 0.f);
-        a.logits[at + e] = l[i];
-      } else {
-        l[i] = a.logits[at + e];
-      }
-    }
-  }
+  for (int i = 0; i < EPL; ++i) l[i] = 0.f;
+#pragma unroll 4
+  for (int z = 0; z < nz; ++z)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] += src[z * part + at + min(lane + kWave * i, a.E - 1)];
+  if (a.parts && a.bias)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] += a.bias[min(lane + kWave * i, a.E - 1)];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (lane + kWave * i >= a.E) l[i] = -INFINITY;
 }
 template <int EPL>
 __device__ __forceinline__ void softmax_row(float (&l)[EPL]) {
@@ -374,11 +489,30 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
     if (lane == 0) a.ntok[chunk + b] = n;
   };
   reset();
+  // all of the wave's rows are requested before the first is used
+  float rows[kChunkTokens][EPL];
+  int slots[kChunkTokens];  // slot j in lane j
+#pragma unroll
+  for (int i = 0; i < kChunkTokens; ++i) {
+    const int t = min(t0 + i, t1 - 1);
+    load_row<EPL>(a, t, rows[i]);
+    slots[i] = lane < a.K ? a.idx[int64_t(t) * a.K + lane] : -1;
+  }
+  if (a.parts) {  // (after all loads: the compiler cannot tell that the arrays differ)
+#pragma unroll
+    for (int q = 0; q < kChunkTokens; ++q)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + kWave * i;
+        if (t0 + q < t1 && e < a.E) a.logits[int64_t(t0 + q) * a.E + e] = rows[q][i];
+      }
+  }
   int b = -1;
-  for (int t = t0; t < t1; ++t) {
-    float l[EPL];
-    load_row<EPL>(a, t, l);
-    if (t < lo || t >= hi) continue;
+#pragma unroll
+  for (int q = 0; q < kChunkTokens; ++q) {
+    const int t = t0 + q;
+    float(&l)[EPL] = rows[q];
+    if (t >= t1 || t < lo || t >= hi) continue;
     const int tb = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t));
     if (tb != b) {
       if (b >= 0) flush(b), reset();
@@ -390,7 +524,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sum[i] += l[i];
     for (int j = 0; j < a.K; ++j) {
-      const int e = a.idx[int64_t(t) * a.K + j];
+      const int e = read_lane_i(slots[q], j);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) cnt[i] += e == lane + kWave * i && e < a.E;
     }
@@ -448,6 +582,7 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(FinishAr
   if (lane == 0) {
     a.terms[b * gridDim.x + blockIdx.x] = term;
     if (blockIdx.x == 0) a.seq_tokens[b] = n;
+    if (gridDim.x * gridDim.y == 1) a.loss[0] = n ? term * (float(a.E) / (float(a.K) * float(n))) : 0.f;
   }
 }
 
@@ -482,14 +617,28 @@ __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
   float db[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) db[i] = 0.f;
-  for (int t = t0; t < t1; ++t) {
+  // all of the wave's rows are requested before the first is used
+  float rows[kChunkTokens][EPL];
+  int slots[kChunkTokens];  // slot j in lane j
+  float dws[kChunkTokens];
+#pragma unroll
+  for (int i = 0; i < kChunkTokens; ++i) {
+    const int t = min(t0 + i, t1 - 1);
+    load_row<EPL>(a, t, rows[i]);
+    const int64_t at = int64_t(t) * a.K + min(lane, a.K - 1);
+    slots[i] = a.dtopk && lane < a.K ? a.idx[at] : -1;
+    dws[i] = a.dtopk ? a.dtopk[at] : 0.f;
+  }
+#pragma unroll
+  for (int q = 0; q < kChunkTokens; ++q) {
+    const int t = t0 + q;
+    if (t >= t1) continue;
     const bool on = t >= lo && t < hi && (!a.tokens.mask || a.tokens.mask[t]);
     float d[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) d[i] = 0.f;
     if (on) {
-      float p[EPL];
-      load_row<EPL>(a, t, p);
+      float(&p)[EPL] = rows[q];
       softmax_row<EPL>(p);
       const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t));
       const int n = a.seq_tokens[b];
@@ -507,10 +656,8 @@ __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
       float add = 0.f;
       int slot = -1;
       if (a.dtopk) {
-        const bool has = lane < a.K;
-        slot = has ? a.idx[int64_t(t) * a.K + lane] : -1;
-        if (unsigned(slot) >= unsigned(a.E)) slot = -1;
-        const float dw = slot >= 0 ? a.dtopk[int64_t(t) * a.K + lane] : 0.f;
+        slot = unsigned(slots[q]) < unsigned(a.E) ? slots[q] : -1;
+        const float dw = slot >= 0 ? dws[q] : 0.f;
         if (a.renorm) {
           const float l = slot >= 0 ? a.logits[int64_t(t) * a.E + slot] : -INFINITY;
           const float m = wave_max(l);
@@ -543,7 +690,13 @@ __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = lane + kWave * i;
-      if (e < a.ld) a.dl[int64_t(t) * a.ld + e] = d[i];
+      if (e < a.ld) {
+        uint32_t w[kPieces];
+        split<kPieces>(e < a.E ? d[i] : 0.f, w);
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c)
+          a.dl[(int64_t(c) * a.tokens.T + t) * a.ld + e] = uint16_t(w[c]);
+      }
       db[i] += d[i];
     }
   }
@@ -582,20 +735,21 @@ __global__ __launch_bounds__(kFinishThreads) void sum_chunks_kernel(const float 
 }
 
 int chunks_of(int32_t T) { return (T + kChunkTokens - 1) / kChunkTokens; }
-int tiles_of(int64_t n) { return int((n + kTile - 1) / kTile); }
+int tiles_of(int64_t n, int tile = kTile) { return int((n + tile - 1) / tile); }
 
 // Parts of a reduction of `steps` steps over `tiles` output tiles: enough
-// workgroups for the GPU's 256 CUs, at least `least` steps each.
-int parts_of(int64_t tiles, int steps, int want, int least) {
+// workgroups to keep several on each of the GPU's 256 CUs, at least `least`
+// steps each.
+int parts_of(int64_t tiles, int steps, int least) {
   int z = 1;
-  while (tiles * z < want && steps >= 2 * z * least && z < 32) z *= 2;
+  while (tiles * z < 1024 && steps >= 2 * z * least && z < 32) z *= 2;
   return z;
 }
 int logit_parts(const moe_layer_desc *d, int32_t T) {
-  return parts_of(int64_t(tiles_of(T)) * tiles_of(d->n_experts), tiles_of(d->d_model), 256, 2);
+  return parts_of(int64_t(tiles_of(T)) * tiles_of(d->n_experts), tiles_of(d->d_model, kStep), 4);
 }
 int router_parts(const moe_layer_desc *d, int32_t T) {
-  return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T), 512, 4);
+  return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T, kStep), 4);
 }
 
 template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK>
@@ -603,8 +757,15 @@ void launch_gemm(GemmArgs g, int parts, hipStream_t s) {
   const int steps = (g.K + kStep - 1) / kStep;
   g.per = (steps + parts - 1) / parts;
   g.part = int64_t(g.a.rows) * g.b.rows;
-  launch((split_gemm_kernel<DTA, KCA, DTB, KCB, NATIVE, MASK>),
-         dim3(unsigned(tiles_of(g.b.rows)), unsigned(tiles_of(g.a.rows)), unsigned(parts)), dim3(kThreads), 0, s, g);
+  const dim3 grid(unsigned(tiles_of(g.b.rows)), unsigned(tiles_of(g.a.rows)), unsigned(parts));
+  if constexpr (DTB == kDtPieces) {
+    launch((split_gemm_kernel<DTA, KCA, DTB, KCB, NATIVE, MASK, true>), grid, dim3(kThreads), 0, s, g);
+  } else {
+    if (g.b.vec)
+      launch((split_gemm_kernel<DTA, KCA, DTB, KCB, NATIVE, MASK, true>), grid, dim3(kThreads), 0, s, g);
+    else
+      launch((split_gemm_kernel<DTA, KCA, DTB, KCB, NATIVE, MASK, false>), grid, dim3(kThreads), 0, s, g);
+  }
 }
 
 template <typename F>
@@ -651,8 +812,8 @@ BalanceWorkspace balance_workspace_layout(const moe_layer_desc *d, int32_t T, in
   const size_t fwd = o;
   o = 0;
   const int zw = router_parts(d, T);
-  b.ld = int((E + 3) / 4 * 4);
-  b.dl = take(size_t(T) * b.ld * 4);
+  b.ld = int((E + 7) / 8 * 8);
+  b.dl = take(size_t(kPieces) * T * b.ld * 2);
   b.dwp = take(zw > 1 ? size_t(zw) * D * E * 4 : 0);
   b.dbp = take(size_t(chunks_of(T)) * E * 4);
   b.total = std::max(std::max(fwd, o), size_t(256));
@@ -692,7 +853,7 @@ void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, cons
                counts, seq_tokens, mean, at<float>(ws, L.terms), loss};
   const int blocks = (E + kWave - 1) / kWave;
   launch(balance_finish_kernel, dim3(blocks, n_seqs), dim3(kFinishThreads), 0, s, f);
-  launch(balance_loss_kernel, dim3(1), dim3(kWave), 0, s, f, blocks);
+  if (blocks * n_seqs > 1) launch(balance_loss_kernel, dim3(1), dim3(kWave), 0, s, f, blocks);
 }
 
 void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, const void *w_router,
@@ -704,24 +865,24 @@ void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, 
   const int E = d->n_experts, D = d->d_model;
   const BalanceWorkspace L = balance_workspace_layout(d, T, n_seqs);
   const Tokens tk{mask, seq_off, n_seqs, T};
-  float *dl = at<float>(ws, L.dl);
+  const Operand dl{at<void>(ws, L.dl), L.ld, T, 1, int64_t(T) * L.ld};
   if (T > 0) {
     RowArgs r{};
     r.tokens = tk, r.E = E, r.K = d->top_k;
     r.logits = const_cast<float *>(logits), r.idx = topk_idx;
     r.counts = counts, r.seq_tokens = seq_tokens, r.dloss = dloss, r.dtopk = dtopk_w, r.renorm = d->renormalize;
-    r.dl = dl, r.ld = L.ld, r.dbias = dbias ? at<float>(ws, L.dbp) : nullptr;
+    r.dl = at<uint16_t>(ws, L.dl), r.ld = L.ld, r.dbias = dbias ? at<float>(ws, L.dbp) : nullptr;
     by_experts(E, [&](auto n) {
       launch((balance_dlogits_kernel<decltype(n)::value>), dim3((chunks_of(T) + 3) / 4), dim3(kThreads), 0, s, r);
     });
     if (dx) {
       GemmArgs g{};
-      g.a = Operand{dl, L.ld, T, 1};
+      g.a = dl;
       const int esz = int(act_bytes(d));
       g.b = Operand{w_router, E, D, E % (16 / esz) == 0};
       g.K = E, g.out = dx;
       by_dtype(d->act_dtype, [&](auto dt) {
-        launch_gemm<kDtF32, true, decltype(dt)::value, true, false, false>(g, 1, s);
+        launch_gemm<kDtPieces, true, decltype(dt)::value, true, false, false>(g, 1, s);
       });
     }
   }
@@ -729,11 +890,12 @@ void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, 
     const int z = router_parts(d, T);
     GemmArgs g{};
     g.a = x_operand(d, T, x, false);
-    g.b = Operand{dl, L.ld, E, 1};
+    g.b = dl;
+    g.b.rows = E;
     g.K = T, g.out = z > 1 ? at<float>(ws, L.dwp) : dw;
     g.tokens = tk;
     by_dtype(d->act_dtype, [&](auto dt) {
-      launch_gemm<decltype(dt)::value, false, kDtF32, false, false, true>(g, z, s);
+      launch_gemm<decltype(dt)::value, false, kDtPieces, false, false, true>(g, z, s);
     });
     if (z > 1) {
       const int64_t n = int64_t(D) * E;

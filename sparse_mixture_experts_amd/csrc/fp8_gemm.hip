@@ -880,7 +880,7 @@ void launch_decode(const Fp8Args &a, int64_t tiles, hipStream_t s) {
 // workgroups fit the GPU at once, or experts would leave a larger tile half
 // empty; 256 from two of its tiles per CU on.
 int fp8_tile_rows(int64_t rows, int32_t N, int32_t K, int experts, bool exact) {
-  const int64_t t16 = most_tiles(rows, experts, 16), t64 = most_tiles(rows, experts, 64);
+  const int64_t t16 = most_tiles(rows, experts, 16), t64 = rows / 64 + experts / 2;
   const int dc = decode_cols(K, false), nbx = (N + kBN - 1) / kBN;
   if (rows <= 16LL * experts || t16 * ((N + dc - 1) / dc) <= 2560) return 16;
   if (exact || rows < 96LL * experts || t64 * nbx <= 640) return 64;

@@ -340,7 +340,7 @@ constexpr int kMaxSeqs = 4096;
 struct BalanceWorkspace {
   size_t parts;                     // forward: [z][T][E] partial logits (z > 1)
   size_t psum, count, ntok, terms;  // records per (chunk of tokens, sequence); loss terms
-  size_t dl, dwp, dbp;              // backward: [T][ld] logit gradients, [z][D][E] (z > 1), [chunks][E]
+  size_t dl, dwp, dbp;              // backward: [3][T][ld] logit gradients, [z][D][E] (z > 1), [chunks][E]
   int ld;
   size_t total;
 };
