@@ -38,8 +38,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 64;             // output rows and columns per workgroup
 constexpr int kStep = 64;             // reduction elements per LDS stage
-constexpr int kLds = kStep + 8;       // 16-bit elements per LDS row: 16 rows' 16-byte pieces on different banks
-constexpr int kChunkTokens = 4;       // tokens per wave of the row kernels
 constexpr int kPieces = 3;            // bf16 pieces of an fp32 value
 constexpr int kDtPieces = 3;          // operand type: three bf16 planes (beside the moe_dtype values)
 
@@ -77,6 +75,15 @@ struct GemmArgs {
   Tokens tokens;       // MASK: reduction elements that take part
 };
 
+// Place of element (row, k) in a 64 x 64 tile of 16-bit elements in LDS.  The
+// 16-byte pieces of a row are exchanged by its number so that both the reads
+// (one piece each of 8 neighbouring rows) and the writes of turned-around
+// elements (8 bytes each of every fourth row) meet different banks.
+__device__ __forceinline__ int lds_at(int row, int k) {
+  const int f = ((row >> 2) & 1) | ((((row >> 1) ^ (row >> 3)) & 1) << 1) | (((row >> 4) & 1) << 2);
+  return row * kStep + (((k >> 3) ^ f) << 3) + (k & 7);
+}
+
 template <int DT>
 constexpr int pieces(bool native) {
   return DT == kDtBF16 || native ? 1 : DT == kDtF16 ? 2 : kPieces;
@@ -112,6 +119,10 @@ __device__ __forceinline__ void split(float v, uint32_t (&out)[P]) {
 // stay in flight in between.  Reduction elements that do not exist (or do not
 // take part) are zeroed there; rows that do not exist are not: they reach
 // only results that are not stored.
+// The last step of a reduction that is no multiple of 64 loads its last 64
+// elements and zeroes those of the step before (`start` is where a step's
+// loads begin, the same for both operands), so that a thread's offsets from
+// there never change and cost no multiplication per step.
 // VEC: rows are 16-byte aligned (16-bit KC and fp32: whole 16-byte pieces;
 // 16-bit rows side by side: 8-byte ones).
 template <int DT, bool KC, bool NATIVE, bool VEC>
@@ -122,39 +133,41 @@ struct Stage {
   uint32_t w[W];
   uint32_t on;  // bit j: reduction element j of the four takes part
   template <bool MASK>
-  __device__ __forceinline__ void load(const Operand &o, int row0, int k0, int K, const Tokens &tk, int lo, int hi) {
+  __device__ __forceinline__ void load(const Operand &o, int row0, int start, int K, const Tokens &tk, int lo,
+                                       int hi) {
     const int tid = threadIdx.x;
-    const float *pf = static_cast<const float *>(o.p);
-    const uint16_t *ph = static_cast<const uint16_t *>(o.p);
+    const int64_t from = KC ? int64_t(start) : int64_t(start) * o.ld;  // uniform
+    const float *pf = static_cast<const float *>(o.p) + from;
+    const uint16_t *ph = static_cast<const uint16_t *>(o.p) + from;
     if constexpr (KC) {
       const int64_t row = int64_t(min(row0 + tid / 4, o.rows - 1)) * o.ld;
-      const int k = k0 + tid % 4 * 16;
+      const int c = tid % 4 * 16;
       if constexpr (!VEC) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) w[u] = word(pf, ph, row + min(k + u, K - 1));
+        for (int u = 0; u < 16; ++u) w[u] = word(pf, ph, row + min(c + u, K - 1 - start));
       } else {
         constexpr int C = DT == kDtF32 ? 4 : 8;  // elements of a 16-byte piece
 #pragma unroll
         for (int u = 0; u < 16 / C; ++u) {
-          const int64_t at = row + min(k + C * u, K - C);
+          const int64_t at = row + min(c + C * u, K - C);  // (K < 64: start is 0)
           const uint4 q = DT == kDtF32 ? *reinterpret_cast<const uint4 *>(pf + at)
                                        : *reinterpret_cast<const uint4 *>(ph + at);
           w[4 * u] = q.x, w[4 * u + 1] = q.y, w[4 * u + 2] = q.z, w[4 * u + 3] = q.w;
         }
       }
     } else {
-      const int k = k0 + tid / 16 * 4, r = row0 + tid % 16 * 4;
+      const int c = tid / 16 * 4, r = row0 + tid % 16 * 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t at = int64_t(min(k + j, K - 1)) * o.ld;
+        const uint32_t at = uint32_t(min(c + j, K - 1)) * uint32_t(o.ld);
         if constexpr (!VEC) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) w[4 * j + u] = word(pf, ph, at + min(r + u, o.rows - 1));
+          for (int u = 0; u < 4; ++u) w[4 * j + u] = word(pf, ph, at + uint32_t(min(r + u, o.rows - 1)));
         } else if constexpr (DT == kDtF32) {
-          const uint4 q = *reinterpret_cast<const uint4 *>(pf + at + min(r, o.rows - 4));
+          const uint4 q = *reinterpret_cast<const uint4 *>(pf + (at + uint32_t(min(r, o.rows - 4))));
           w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
         } else {
-          const uint2 q = *reinterpret_cast<const uint2 *>(ph + at + min(r, o.rows - 4));
+          const uint2 q = *reinterpret_cast<const uint2 *>(ph + (at + uint32_t(min(r, o.rows - 4))));
           w[2 * j] = q.x, w[2 * j + 1] = q.y;
         }
       }
@@ -163,11 +176,11 @@ struct Stage {
         if (tk.mask) {
           on = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) on |= uint32_t(tk.mask[min(k + j, K - 1)] != 0) << j;
+          for (int j = 0; j < 4; ++j) on |= uint32_t(tk.mask[start + min(c + j, K - 1)] != 0) << j;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (k + j < lo || k + j >= hi) on &= ~(1u << j);
+          if (start + c + j < lo || start + c + j >= hi) on &= ~(1u << j);
       }
     }
   }
@@ -185,35 +198,38 @@ struct Stage {
     else if constexpr (DT == kDtF32) split<P>(ok ? __uint_as_float(w[u]) : 0.f, q);
     else split<P>(ok ? half_to_f32<DT>(half_bits(u)) : 0.f, q);
   }
-  // into LDS rows row0 .. row0 + 63; k0, K as loaded
-  template <int ROWS>
-  __device__ __forceinline__ void store(uint16_t (&lds)[P][ROWS][kLds], int row0, int k0, int K) const {
+  // into LDS; the elements k0 <= k < K of those loaded from start
+  __device__ __forceinline__ void store(uint16_t (&lds)[P][kTile * kStep], int start, int k0, int K) const {
     const int tid = threadIdx.x;
     if constexpr (KC) {
-      const int k = k0 + tid % 4 * 16;
+      const int k = start + tid % 4 * 16;
       uint32_t o[P][8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        if constexpr (RAW && W == 8) {
-          o[0][u] = k + (u / 4) * 8 < K ? w[u] : 0u;  // K is a multiple of 8
+        if constexpr (RAW && W == 8) {  // K and start are multiples of 8
+          const int c = k + u / 4 * 8;
+          o[0][u] = c >= k0 && c < K ? w[u] : 0u;
         } else {
+          const int c = k + 2 * u;
           uint32_t x[P], y[P];
-          cut(2 * u, k + 2 * u < K, x), cut(2 * u + 1, k + 2 * u + 1 < K, y);
+          cut(2 * u, c >= k0 && c < K, x), cut(2 * u + 1, c + 1 >= k0 && c + 1 < K, y);
 #pragma unroll
           for (int p = 0; p < P; ++p) o[p][u] = x[p] | (y[p] << 16);
         }
       }
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        uint4 *q = reinterpret_cast<uint4 *>(&lds[p][row0 + tid / 4][tid % 4 * 16]);
-        q[0] = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
-        q[1] = make_uint4(o[p][4], o[p][5], o[p][6], o[p][7]);
+        uint16_t *q = lds[p];
+        *reinterpret_cast<uint4 *>(q + lds_at(tid / 4, tid % 4 * 16)) =
+            make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+        *reinterpret_cast<uint4 *>(q + lds_at(tid / 4, tid % 4 * 16 + 8)) =
+            make_uint4(o[p][4], o[p][5], o[p][6], o[p][7]);
       }
     } else {
-      const int k = k0 + tid / 16 * 4;
+      const int k = start + tid / 16 * 4;
       bool ok[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ok[j] = k + j < K && ((on >> j) & 1u);
+      for (int j = 0; j < 4; ++j) ok[j] = k + j >= k0 && k + j < K && ((on >> j) & 1u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // row i of the four
         uint32_t x[4][P];
@@ -221,7 +237,7 @@ struct Stage {
         for (int j = 0; j < 4; ++j) cut(4 * j + i, ok[j], x[j]);
 #pragma unroll
         for (int p = 0; p < P; ++p)
-          *reinterpret_cast<uint2 *>(&lds[p][row0 + tid % 16 * 4 + i][tid / 16 * 4]) =
+          *reinterpret_cast<uint2 *>(&lds[p][lds_at(tid % 16 * 4 + i, tid / 16 * 4)]) =
               make_uint2(x[0][p] | (x[1][p] << 16), x[2][p] | (x[3][p] << 16));
       }
     }
@@ -234,51 +250,53 @@ struct Stage<kDtPieces, KC, false, true> {
   static constexpr int P = kPieces;
   uint32_t w[P][8];  // (words: arrays of vectors here went to scratch memory)
   template <bool MASK>
-  __device__ __forceinline__ void load(const Operand &o, int row0, int k0, int K, const Tokens &, int, int) {
+  __device__ __forceinline__ void load(const Operand &o, int row0, int start, int K, const Tokens &, int, int) {
     const int tid = threadIdx.x;
-    const uint16_t *base = static_cast<const uint16_t *>(o.p);
     if constexpr (KC) {  // 16 elements of a row
+      const uint16_t *base = static_cast<const uint16_t *>(o.p) + start;
       const int64_t row = int64_t(min(row0 + tid / 4, o.rows - 1)) * o.ld;
-      const int k = k0 + tid % 4 * 16;
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 q = *reinterpret_cast<const uint4 *>(base + p * o.plane + row + min(k + 8 * h, int(o.ld) - 8));
+          const int c = min(tid % 4 * 16 + 8 * h, int(o.ld) - 8);
+          const uint4 q = *reinterpret_cast<const uint4 *>(base + p * o.plane + (row + c));
           w[p][4 * h] = q.x, w[p][4 * h + 1] = q.y, w[p][4 * h + 2] = q.z, w[p][4 * h + 3] = q.w;
         }
     } else {  // 4 x 4 elements, two words for each reduction element
-      const int k = k0 + tid / 16 * 4, r = min(row0 + tid % 16 * 4, int(o.ld) - 4);
+      const uint16_t *base = static_cast<const uint16_t *>(o.p) + int64_t(start) * o.ld;
+      const int c = tid / 16 * 4, r = min(row0 + tid % 16 * 4, int(o.ld) - 4);
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint2 q =
-              *reinterpret_cast<const uint2 *>(base + p * o.plane + int64_t(min(k + j, K - 1)) * o.ld + r);
+          const uint32_t at = uint32_t(min(c + j, K - 1)) * uint32_t(o.ld) + uint32_t(r);
+          const uint2 q = *reinterpret_cast<const uint2 *>(base + p * o.plane + at);
           w[p][2 * j] = q.x, w[p][2 * j + 1] = q.y;
         }
     }
   }
-  template <int ROWS>
-  __device__ __forceinline__ void store(uint16_t (&lds)[P][ROWS][kLds], int row0, int k0, int K) const {
+  __device__ __forceinline__ void store(uint16_t (&lds)[P][kTile * kStep], int start, int k0, int K) const {
     const int tid = threadIdx.x;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       if constexpr (KC) {  // (elements past K, up to a multiple of 8, are zero in memory)
-        const int k = k0 + tid % 4 * 16;
-        uint4 *q = reinterpret_cast<uint4 *>(&lds[p][row0 + tid / 4][tid % 4 * 16]);
-        const bool a = k < K, b = k + 8 < K;
-        q[0] = make_uint4(a ? w[p][0] : 0u, a ? w[p][1] : 0u, a ? w[p][2] : 0u, a ? w[p][3] : 0u);
-        q[1] = make_uint4(b ? w[p][4] : 0u, b ? w[p][5] : 0u, b ? w[p][6] : 0u, b ? w[p][7] : 0u);
+        const int k = start + tid % 4 * 16;
+        uint16_t *q = lds[p];
+        const bool a = k >= k0 && k < K, b = k + 8 >= k0 && k + 8 < K;
+        *reinterpret_cast<uint4 *>(q + lds_at(tid / 4, tid % 4 * 16)) =
+            make_uint4(a ? w[p][0] : 0u, a ? w[p][1] : 0u, a ? w[p][2] : 0u, a ? w[p][3] : 0u);
+        *reinterpret_cast<uint4 *>(q + lds_at(tid / 4, tid % 4 * 16 + 8)) =
+            make_uint4(b ? w[p][4] : 0u, b ? w[p][5] : 0u, b ? w[p][6] : 0u, b ? w[p][7] : 0u);
       } else {
-        const int k = k0 + tid / 16 * 4;
+        const int k = start + tid / 16 * 4;
         uint32_t v[8];  // [reduction element][pair of rows]
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = k + j / 2 < K ? w[p][j] : 0u;
+        for (int j = 0; j < 8; ++j) v[j] = k + j / 2 >= k0 && k + j / 2 < K ? w[p][j] : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;  // high or low halves of two words
-          *reinterpret_cast<uint2 *>(&lds[p][row0 + tid % 16 * 4 + i][tid / 16 * 4]) =
+          *reinterpret_cast<uint2 *>(&lds[p][lds_at(tid % 16 * 4 + i, tid / 16 * 4)]) =
               make_uint2(__builtin_amdgcn_perm(v[2 + (i >> 1)], v[i >> 1], sel),
                          __builtin_amdgcn_perm(v[6 + (i >> 1)], v[4 + (i >> 1)], sel));
         }
@@ -297,10 +315,10 @@ template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK, bool VEC
 __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
   using SA = Stage<DTA, KCA, NATIVE, true>;
   using SB = Stage<DTB, KCB, NATIVE, VECB>;
-  constexpr int PA = SA::P, PB = SB::P, S = 2, TILE = kTile;
-  __shared__ __align__(16) uint16_t la[PA][TILE][kLds], lb[PB][TILE][kLds];
+  constexpr int PA = SA::P, PB = SB::P, S = 2;
+  __shared__ __align__(16) uint16_t la[PA][kTile * kStep], lb[PB][kTile * kStep];
   const int lane = lane_id(), wave = threadIdx.x / kWave, lr = lane & 15, lg = lane >> 4;
-  const int m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE;
+  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
   const int wm = (wave >> 1) * 16 * S, wn = (wave & 1) * 16 * S;
   const int s0 = int(blockIdx.z) * g.per, s1 = min(s0 + g.per, (g.K + kStep - 1) / kStep);
   int lo = 0, hi = 0;
@@ -312,16 +330,20 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
     for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   SA sa[2];
   SB sb[2];
+  // where step s loads from: its own elements, or the last 64 (a multiple of
+  // 8 where both operands are read along the reduction)
+  const int Kl = KCA && KCB ? (g.K + 7) / 8 * 8 : g.K;
+  auto start_of = [&](int s) { return max(0, min(s * kStep, Kl - kStep)); };
   auto load = [&](int s, auto rc) {
     constexpr int r = decltype(rc)::value;
-    sa[r].template load<MASK>(g.a, m0, s * kStep, g.K, g.tokens, lo, hi);
-    sb[r].template load<MASK>(g.b, n0, s * kStep, g.K, g.tokens, lo, hi);
+    sa[r].template load<MASK>(g.a, m0, start_of(s), g.K, g.tokens, lo, hi);
+    sb[r].template load<MASK>(g.b, n0, start_of(s), g.K, g.tokens, lo, hi);
   };
   auto step = [&](int s, auto rc) {
     constexpr int r = decltype(rc)::value;
     __syncthreads();
-    sa[r].store(la, 0, s * kStep, g.K);
-    sb[r].store(lb, 0, s * kStep, g.K);
+    sa[r].store(la, start_of(s), s * kStep, g.K);
+    sb[r].store(lb, start_of(s), s * kStep, g.K);
     __syncthreads();
     if (s + 2 < s1) load(s + 2, rc);
 #pragma unroll
@@ -331,12 +353,12 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
       for (int p = 0; p < PA; ++p)
 #pragma unroll
         for (int i = 0; i < S; ++i)
-          fa[p][i] = *reinterpret_cast<const uint4 *>(&la[p][wm + i * 16 + lr][kk + lg * 8]);
+          fa[p][i] = *reinterpret_cast<const uint4 *>(&la[p][lds_at(wm + i * 16 + lr, kk + lg * 8)]);
 #pragma unroll
       for (int q = PB - 1; q >= 0; --q)
 #pragma unroll
         for (int j = 0; j < S; ++j) {
-          const uint4 fb = *reinterpret_cast<const uint4 *>(&lb[q][wn + j * 16 + lr][kk + lg * 8]);
+          const uint4 fb = *reinterpret_cast<const uint4 *>(&lb[q][lds_at(wn + j * 16 + lr, kk + lg * 8)]);
 #pragma unroll
           for (int p = PA - 1; p >= 0; --p)
             if (p + q < kPieces)
@@ -405,6 +427,7 @@ __device__ __forceinline__ int sequence_of(const Tokens &k, int t) {
 struct RowArgs {
   Tokens tokens;
   int E, K;
+  int chunk;               // tokens per workgroup
   const float *parts;      // [z][T][E] partial logits, or null: `logits` holds them
   int z;
   const float *bias;       // added to the parts
@@ -424,25 +447,43 @@ struct RowArgs {
   float *dbias;            // [chunks][E] partial sums, or null
 };
 
-// Experts lane, lane + 64, ... of one token's logits; -inf past the end.
+constexpr int kRowWaves = kThreads / kWave;
+constexpr int kPair = 2;  // tokens that a wave takes at a time, all their loads in flight together
+
+// Experts lane, lane + 64, ... of the logits of tokens t and t + 1 (up to
+// t1 - 1); -inf past the end.  Partial logits are summed in their order.
 template <int EPL>
-__device__ __forceinline__ void load_row(const RowArgs &a, int t, float (&l)[EPL]) {
+__device__ __forceinline__ void load_rows(const RowArgs &a, int t, int t1, float (&l)[kPair][EPL]) {
   const int lane = lane_id();
-  const int64_t at = int64_t(t) * a.E, part = int64_t(a.tokens.T) * a.E;
+  const int64_t part = int64_t(a.tokens.T) * a.E;
   const float *src = a.parts ? a.parts : a.logits;
   const int nz = a.parts ? a.z : 1;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) l[i] = 0.f;
-#pragma unroll 4
+  for (int q = 0; q < kPair; ++q)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[q][i] = a.parts && a.bias ? a.bias[min(lane + kWave * i, a.E - 1)] : 0.f;
+  // (the bias first: its place in the sum is free, its loads are not waited for)
+#pragma unroll 2
   for (int z = 0; z < nz; ++z)
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] += src[z * part + at + min(lane + kWave * i, a.E - 1)];
-  if (a.parts && a.bias)
+    for (int q = 0; q < kPair; ++q)
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] += a.bias[min(lane + kWave * i, a.E - 1)];
+      for (int i = 0; i < EPL; ++i)
+        l[q][i] += src[z * part + int64_t(min(t + q, t1 - 1)) * a.E + min(lane + kWave * i, a.E - 1)];
+  if (a.parts) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    if (lane + kWave * i >= a.E) l[i] = -INFINITY;
+    for (int q = 0; q < kPair; ++q)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + kWave * i;
+        if (t + q < t1 && e < a.E) a.logits[int64_t(t + q) * a.E + e] = l[q][i];
+      }
+  }
+#pragma unroll
+  for (int q = 0; q < kPair; ++q)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (lane + kWave * i >= a.E) l[q][i] = -INFINITY;
 }
 template <int EPL>
 __device__ __forceinline__ void softmax_row(float (&l)[EPL]) {
@@ -461,80 +502,73 @@ __device__ __forceinline__ void softmax_row(float (&l)[EPL]) {
   for (int i = 0; i < EPL; ++i) l[i] *= r;
 }
 
-// Forward: a wave takes kChunkTokens consecutive tokens and leaves, for every
-// sequence among them, the sums of its counted tokens' probabilities and the
-// counts of their slots.
+// Forward: a workgroup takes a chunk of consecutive tokens and leaves, for
+// every sequence among them, the sums of its counted tokens' probabilities
+// and the counts of their slots, at place chunk number + sequence number
+// (which no other pair shares).
 template <int EPL>
 __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
-  const int chunk = int(blockIdx.x) * (kThreads / kWave) + int(threadIdx.x) / kWave;
-  const int t0 = chunk * kChunkTokens, t1 = min(t0 + kChunkTokens, a.tokens.T);
-  if (t0 >= t1) return;
-  const int lane = lane_id();
+  __shared__ float ps[kRowWaves][EPL * kWave];
+  __shared__ int32_t cs[kRowWaves][EPL * kWave], ns[kRowWaves];
+  const int c0 = int(blockIdx.x) * a.chunk, c1 = min(c0 + a.chunk, a.tokens.T);
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int lo, hi;
   token_range(a.tokens, lo, hi);
-  float sum[EPL];
-  int32_t cnt[EPL], n = 0;
-  auto reset = [&]() {
+  lo = min(max(lo, c0), c1), hi = max(min(hi, c1), lo);
+  float l[kPair][EPL];
+  if (a.parts) {  // tokens of no sequence: their logits alone
+    for (int t = c0 + kPair * wave; t < lo; t += kPair * kRowWaves) load_rows<EPL>(a, t, lo, l);
+    for (int t = hi + kPair * wave; t < c1; t += kPair * kRowWaves) load_rows<EPL>(a, t, c1, l);
+  }
+  for (int t0 = lo; t0 < hi;) {  // one sequence's tokens t0 .. t1 - 1
+    const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t0));
+    const int t1 = a.tokens.off ? max(min(a.tokens.off[b + 1], hi), t0 + 1) : hi;
+    float sum[EPL];
+    int32_t cnt[EPL], n = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
-    n = 0;
-  };
-  auto flush = [&](int b) {
-    const int64_t at = int64_t(chunk + b) * a.E;
+    for (int t = t0 + kPair * wave; t < t1; t += kPair * kRowWaves) {
+      int slot[kPair];  // slot j in lane j
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + kWave * i;
-      if (e < a.E) a.psum[at + e] = sum[i], a.count[at + e] = cnt[i];
-    }
-    if (lane == 0) a.ntok[chunk + b] = n;
-  };
-  reset();
-  // all of the wave's rows are requested before the first is used
-  float rows[kChunkTokens][EPL];
-  int slots[kChunkTokens];  // slot j in lane j
+      for (int q = 0; q < kPair; ++q)
+        slot[q] = a.idx[int64_t(min(t + q, t1 - 1)) * a.K + min(lane, a.K - 1)];
+      load_rows<EPL>(a, t, t1, l);
 #pragma unroll
-  for (int i = 0; i < kChunkTokens; ++i) {
-    const int t = min(t0 + i, t1 - 1);
-    load_row<EPL>(a, t, rows[i]);
-    slots[i] = lane < a.K ? a.idx[int64_t(t) * a.K + lane] : -1;
-  }
-  if (a.parts) {  // (after all loads: the compiler cannot tell that the arrays differ)
+      for (int q = 0; q < kPair; ++q) {
+        if (t + q >= t1 || (a.tokens.mask && !a.tokens.mask[t + q])) continue;
+        softmax_row<EPL>(l[q]);
+        ++n;
 #pragma unroll
-    for (int q = 0; q < kChunkTokens; ++q)
+        for (int i = 0; i < EPL; ++i) sum[i] += l[q][i];
+        for (int j = 0; j < a.K; ++j) {
+          const int e = read_lane_i(slot[q], j);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = lane + kWave * i;
-        if (t0 + q < t1 && e < a.E) a.logits[int64_t(t0 + q) * a.E + e] = rows[q][i];
+          for (int i = 0; i < EPL; ++i) cnt[i] += e == lane + kWave * i;
+        }
       }
-  }
-  int b = -1;
-#pragma unroll
-  for (int q = 0; q < kChunkTokens; ++q) {
-    const int t = t0 + q;
-    float(&l)[EPL] = rows[q];
-    if (t >= t1 || t < lo || t >= hi) continue;
-    const int tb = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t));
-    if (tb != b) {
-      if (b >= 0) flush(b), reset();
-      b = tb;
     }
-    if (a.tokens.mask && !a.tokens.mask[t]) continue;
-    softmax_row<EPL>(l);
-    ++n;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sum[i] += l[i];
-    for (int j = 0; j < a.K; ++j) {
-      const int e = read_lane_i(slots[q], j);
+    for (int i = 0; i < EPL; ++i) ps[wave][lane + kWave * i] = sum[i], cs[wave][lane + kWave * i] = cnt[i];
+    if (lane == 0) ns[wave] = n;
+    __syncthreads();
+    const int64_t at = int64_t(blockIdx.x) + b;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+      float p = ps[0][e];
+      int32_t c = cs[0][e];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) cnt[i] += e == lane + kWave * i && e < a.E;
+      for (int w = 1; w < kRowWaves; ++w) p += ps[w][e], c += cs[w][e];
+      a.psum[at * a.E + e] = p;
+      a.count[at * a.E + e] = c;
     }
+    if (threadIdx.x == 0) a.ntok[at] = ns[0] + ns[1] + ns[2] + ns[3];
+    __syncthreads();
+    t0 = t1;
   }
-  if (b >= 0) flush(b);
 }
 
 struct FinishArgs {
   Tokens tokens;
-  int E, K;
+  int E, K, chunk;
   const float *psum;
   const int32_t *count, *ntok;
   int32_t *counts, *seq_tokens;
@@ -557,7 +591,7 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(FinishAr
     lo = min(max(a.tokens.off[b], 0), a.tokens.T);
     hi = min(max(a.tokens.off[b + 1], lo), a.tokens.T);
   }
-  const int c0 = lo / kChunkTokens, c1 = hi > lo ? (hi - 1) / kChunkTokens + 1 : c0;
+  const int c0 = lo / a.chunk, c1 = hi > lo ? (hi - 1) / a.chunk + 1 : c0;
   float p = 0.f;
   int32_t c = 0, n = 0;
 #pragma unroll 8
@@ -601,111 +635,112 @@ __global__ __launch_bounds__(kWave) void balance_loss_kernel(FinishArgs a, int b
   if (lane_id() == 0) a.loss[0] = f > 0.f ? s / f : 0.f;
 }
 
-// Backward of the rows: dl of kChunkTokens tokens per wave, and their sum.
+// Backward of the rows: dl of a chunk of tokens, and their sum.
 template <int EPL>
 __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
-  const int chunk = int(blockIdx.x) * (kThreads / kWave) + int(threadIdx.x) / kWave;
-  const int t0 = chunk * kChunkTokens, t1 = min(t0 + kChunkTokens, a.tokens.T);
-  if (t0 >= t1) return;
-  const int lane = lane_id();
+  __shared__ float ds[kRowWaves][EPL * kWave];
+  const int c0 = int(blockIdx.x) * a.chunk, c1 = min(c0 + a.chunk, a.tokens.T);
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int lo, hi;
   token_range(a.tokens, lo, hi);
   int filled = 0;
   for (int b = lane; b < a.tokens.n; b += kWave) filled += a.seq_tokens[b] > 0;
   const float nf = wave_sum(float(filled));
   const float up = a.dloss ? a.dloss[0] : 1.0f;
-  float db[EPL];
+  float db[EPL], gb[EPL];  // sum of dl; d loss / d p of sequence `of`
+  int of = -1;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) db[i] = 0.f;
-  // all of the wave's rows are requested before the first is used
-  float rows[kChunkTokens][EPL];
-  int slots[kChunkTokens];  // slot j in lane j
-  float dws[kChunkTokens];
+  for (int i = 0; i < EPL; ++i) db[i] = 0.f, gb[i] = 0.f;
+  for (int t = c0 + kPair * wave; t < c1; t += kPair * kRowWaves) {
+    float l[kPair][EPL], dws[kPair], lsel[kPair];
+    int slots[kPair];  // slot j in lane j
 #pragma unroll
-  for (int i = 0; i < kChunkTokens; ++i) {
-    const int t = min(t0 + i, t1 - 1);
-    load_row<EPL>(a, t, rows[i]);
-    const int64_t at = int64_t(t) * a.K + min(lane, a.K - 1);
-    slots[i] = a.dtopk && lane < a.K ? a.idx[at] : -1;
-    dws[i] = a.dtopk ? a.dtopk[at] : 0.f;
-  }
+    for (int q = 0; q < kPair; ++q) {
+      const int64_t tq = min(t + q, c1 - 1);
+      const int64_t at = tq * a.K + min(lane, a.K - 1);
+      slots[q] = a.dtopk ? a.idx[at] : -1;
+      dws[q] = a.dtopk ? a.dtopk[at] : 0.f;
+      if (lane >= a.K || unsigned(slots[q]) >= unsigned(a.E)) slots[q] = -1;
+    }
+    load_rows<EPL>(a, t, c1, l);
 #pragma unroll
-  for (int q = 0; q < kChunkTokens; ++q) {
-    const int t = t0 + q;
-    if (t >= t1) continue;
-    const bool on = t >= lo && t < hi && (!a.tokens.mask || a.tokens.mask[t]);
-    float d[EPL];
+    for (int q = 0; q < kPair; ++q)
+      lsel[q] = a.dtopk ? a.logits[int64_t(min(t + q, c1 - 1)) * a.E + max(slots[q], 0)] : 0.f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) d[i] = 0.f;
-    if (on) {
-      float(&p)[EPL] = rows[q];
-      softmax_row<EPL>(p);
-      const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t));
-      const int n = a.seq_tokens[b];
-      const float fn = float(n);
-      // (a zero n or nf: no token of the forward pass counted; nothing flows)
-      const float coef = n > 0 && nf > 0.f ? up * float(a.E) / (float(a.K) * fn * fn * nf) : 0.f;
-      const int mean = int(int64_t(n) * a.K / a.E);
-      float g[EPL];
+    for (int q = 0; q < kPair; ++q) {
+      if (t + q >= c1) continue;
+      const bool on = t + q >= lo && t + q < hi && (!a.tokens.mask || a.tokens.mask[t + q]);
+      float d[EPL];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = lane + kWave * i;
-        g[i] = e < a.E ? coef * float(a.counts[int64_t(b) * a.E + e] - mean) : 0.f;
-      }
-      // the routing weights' part, slot j in lane j
-      float add = 0.f;
-      int slot = -1;
-      if (a.dtopk) {
-        slot = unsigned(slots[q]) < unsigned(a.E) ? slots[q] : -1;
+      for (int i = 0; i < EPL; ++i) d[i] = 0.f;
+      if (on) {
+        const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t + q));
+        if (b != of) {
+          of = b;
+          const int n = a.seq_tokens[b];
+          const float fn = float(n);
+          // (a zero n or nf: no token of the forward pass counted; nothing flows)
+          const float coef = n > 0 && nf > 0.f ? up * float(a.E) / (float(a.K) * fn * fn * nf) : 0.f;
+          const int mean = int(int64_t(n) * a.K / a.E);
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            gb[i] = coef * float(a.counts[int64_t(b) * a.E + min(lane + kWave * i, a.E - 1)] - mean);
+        }
+        float(&p)[EPL] = l[q];
+        softmax_row<EPL>(p);
+        float g[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) g[i] = gb[i];
+        // the routing weights' part, slot j in lane j
+        const int slot = slots[q];
         const float dw = slot >= 0 ? dws[q] : 0.f;
-        if (a.renorm) {
-          const float l = slot >= 0 ? a.logits[int64_t(t) * a.E + slot] : -INFINITY;
-          const float m = wave_max(l);
-          const float ex = slot >= 0 ? expf(l - m) : 0.f;
+        float add = dw;
+        if (a.dtopk && a.renorm) {
+          const float ls = slot >= 0 ? lsel[q] : -INFINITY;
+          const float m = wave_max(ls);
+          const float ex = slot >= 0 ? expf(ls - m) : 0.f;
           const float w = ex * (1.0f / wave_sum(ex));
           const float s = wave_sum(slot >= 0 ? w * dw : 0.f);
           add = slot >= 0 ? w * (dw - s) : 0.f;
-        } else {
-          add = dw;
         }
-      }
-      auto scatter = [&](float (&to)[EPL]) {
-        for (int j = 0; j < a.K; ++j) {
-          const int e = read_lane_i(slot, j);
-          const float v = read_lane(add, j);
+        auto scatter = [&](float (&to)[EPL]) {
+          for (int j = 0; j < a.K; ++j) {
+            const int e = read_lane_i(slot, j);
+            const float v = read_lane(add, j);
 #pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (e == lane + kWave * i) to[i] += v;
+            for (int i = 0; i < EPL; ++i)
+              if (e == lane + kWave * i) to[i] += v;
+          }
+        };
+        if (a.dtopk && !a.renorm) scatter(g);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) s += p[i] * g[i];
+        s = wave_sum(s);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) d[i] = p[i] * (g[i] - s);
+        if (a.dtopk && a.renorm) scatter(d);
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + kWave * i;
+        if (e < a.ld) {
+          uint32_t w[kPieces];
+          split<kPieces>(e < a.E ? d[i] : 0.f, w);
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c)
+            a.dl[(int64_t(c) * a.tokens.T + t + q) * a.ld + e] = uint16_t(w[c]);
         }
-      };
-      if (a.dtopk && !a.renorm) scatter(g);
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) s += p[i] * g[i];
-      s = wave_sum(s);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) d[i] = p[i] * (g[i] - s);
-      if (a.dtopk && a.renorm) scatter(d);
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + kWave * i;
-      if (e < a.ld) {
-        uint32_t w[kPieces];
-        split<kPieces>(e < a.E ? d[i] : 0.f, w);
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c)
-          a.dl[(int64_t(c) * a.tokens.T + t) * a.ld + e] = uint16_t(w[c]);
+        db[i] += d[i];
       }
-      db[i] += d[i];
     }
   }
   if (a.dbias) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + kWave * i;
-      if (e < a.E) a.dbias[int64_t(chunk) * a.E + e] = db[i];
-    }
+    for (int i = 0; i < EPL; ++i) ds[wave][lane + kWave * i] = db[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
+      a.dbias[int64_t(blockIdx.x) * a.E + e] = ((ds[0][e] + ds[1][e]) + ds[2][e]) + ds[3][e];
   }
 }
 
@@ -734,22 +769,25 @@ __global__ __launch_bounds__(kFinishThreads) void sum_chunks_kernel(const float 
   if (e < E) out[e] = s;
 }
 
-int chunks_of(int32_t T) { return (T + kChunkTokens - 1) / kChunkTokens; }
+// Tokens per workgroup of the row kernels: 8 (two for each wave), more where
+// the chunks would be many more than the GPU takes at once.
+int chunk_tokens(int32_t T) { return T <= 8192 ? 8 : T <= 65536 ? 32 : 128; }
+int chunks_of(int32_t T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
 int tiles_of(int64_t n, int tile = kTile) { return int((n + tile - 1) / tile); }
 
 // Parts of a reduction of `steps` steps over `tiles` output tiles: enough
 // workgroups to keep several on each of the GPU's 256 CUs, at least `least`
 // steps each.
-int parts_of(int64_t tiles, int steps, int least) {
+int parts_of(int64_t tiles, int steps, int want, int least) {
   int z = 1;
-  while (tiles * z < 1024 && steps >= 2 * z * least && z < 32) z *= 2;
+  while (tiles * z < want && steps >= 2 * z * least && z < 32) z *= 2;
   return z;
 }
 int logit_parts(const moe_layer_desc *d, int32_t T) {
-  return parts_of(int64_t(tiles_of(T)) * tiles_of(d->n_experts), tiles_of(d->d_model, kStep), 4);
+  return parts_of(int64_t(tiles_of(T)) * tiles_of(d->n_experts), tiles_of(d->d_model, kStep), 512, 2);
 }
 int router_parts(const moe_layer_desc *d, int32_t T) {
-  return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T, kStep), 4);
+  return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T, kStep), 1024, 4);
 }
 
 template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK>
@@ -841,15 +879,15 @@ void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, cons
       launch_gemm<DT, true, DT, false, DT == kDtF16, false>(g, z, s);
     });
     RowArgs r{};
-    r.tokens = tk, r.E = E, r.K = d->top_k;
+    r.tokens = tk, r.E = E, r.K = d->top_k, r.chunk = chunk_tokens(T);
     r.parts = z > 1 ? at<float>(ws, L.parts) : nullptr, r.z = z, r.bias = bias;
     r.logits = logits, r.idx = topk_idx;
     r.psum = at<float>(ws, L.psum), r.count = at<int32_t>(ws, L.count), r.ntok = at<int32_t>(ws, L.ntok);
     by_experts(E, [&](auto n) {
-      launch((balance_rows_kernel<decltype(n)::value>), dim3((chunks_of(T) + 3) / 4), dim3(kThreads), 0, s, r);
+      launch((balance_rows_kernel<decltype(n)::value>), dim3(chunks_of(T)), dim3(kThreads), 0, s, r);
     });
   }
-  FinishArgs f{tk, E, d->top_k, at<float>(ws, L.psum), at<int32_t>(ws, L.count), at<int32_t>(ws, L.ntok),
+  FinishArgs f{tk, E, d->top_k, chunk_tokens(T), at<float>(ws, L.psum), at<int32_t>(ws, L.count), at<int32_t>(ws, L.ntok),
                counts, seq_tokens, mean, at<float>(ws, L.terms), loss};
   const int blocks = (E + kWave - 1) / kWave;
   launch(balance_finish_kernel, dim3(blocks, n_seqs), dim3(kFinishThreads), 0, s, f);
@@ -868,12 +906,12 @@ void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, 
   const Operand dl{at<void>(ws, L.dl), L.ld, T, 1, int64_t(T) * L.ld};
   if (T > 0) {
     RowArgs r{};
-    r.tokens = tk, r.E = E, r.K = d->top_k;
+    r.tokens = tk, r.E = E, r.K = d->top_k, r.chunk = chunk_tokens(T);
     r.logits = const_cast<float *>(logits), r.idx = topk_idx;
     r.counts = counts, r.seq_tokens = seq_tokens, r.dloss = dloss, r.dtopk = dtopk_w, r.renorm = d->renormalize;
     r.dl = at<uint16_t>(ws, L.dl), r.ld = L.ld, r.dbias = dbias ? at<float>(ws, L.dbp) : nullptr;
     by_experts(E, [&](auto n) {
-      launch((balance_dlogits_kernel<decltype(n)::value>), dim3((chunks_of(T) + 3) / 4), dim3(kThreads), 0, s, r);
+      launch((balance_dlogits_kernel<decltype(n)::value>), dim3(chunks_of(T)), dim3(kThreads), 0, s, r);
     });
     if (dx) {
       GemmArgs g{};
