@@ -73,6 +73,8 @@ struct GemmArgs {
   int64_t part;        // elements per part
   const float *bias;   // nullable, added per column
   Tokens tokens;       // MASK: reduction elements that take part
+  float *bsum = nullptr;  // MASK: sum_k B(n, k), [parts][b.rows] after `bpart` elements each (null: not wanted)
+  int64_t bpart = 0;
 };
 
 // Place of element (row, k) in a 64 x 64 tile of 16-bit elements in LDS.  The
@@ -328,6 +330,13 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
   for (int i = 0; i < S; ++i)
 #pragma unroll
     for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // The sums of B over the reduction are its products with ones, made by the
+  // waves that hold the first rows of the first row of tiles.
+  const bool sums = MASK && g.bsum && m0 == 0 && wm == 0;
+  f32x4 accb[S];
+#pragma unroll
+  for (int j = 0; j < S; ++j) accb[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // bf16 1.0
   SA sa[2];
   SB sb[2];
   // where step s loads from: its own elements, or the last 64 (a multiple of
@@ -359,6 +368,10 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
 #pragma unroll
         for (int j = 0; j < S; ++j) {
           const uint4 fb = *reinterpret_cast<const uint4 *>(&lb[q][lds_at(wn + j * 16 + lr, kk + lg * 8)]);
+          if constexpr (MASK && !NATIVE) {
+            if (sums)
+              accb[j] = mfma_bf16(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, ones), accb[j]);
+          }
 #pragma unroll
           for (int p = PA - 1; p >= 0; --p)
             if (p + q < kPieces)
@@ -385,8 +398,18 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
     }
     if (s < s1) step(s, R0{});
   }
-  float *out = g.out + int64_t(blockIdx.z) * g.part;
   const int N = g.b.rows;
+  if (sums && lr == 0) {  // every column of the product holds the same sums
+#pragma unroll
+    for (int j = 0; j < S; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int n = n0 + wn + j * 16 + 4 * lg + c;
+        if (n < N) g.bsum[int64_t(blockIdx.z) * g.bpart + n] = accb[j][c];
+      }
+  }
+  if (!g.out) return;
+  float *out = g.out + int64_t(blockIdx.z) * g.part;
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     const int m = m0 + wm + i * 16 + lr;
@@ -444,7 +467,6 @@ struct RowArgs {
   int renorm;
   uint16_t *dl;            // bf16 pieces [3][T][ld], zero past E
   int ld;
-  float *dbias;            // [chunks][E] partial sums, or null
 };
 
 constexpr int kRowWaves = kThreads / kWave;
@@ -502,6 +524,35 @@ __device__ __forceinline__ void softmax_row(float (&l)[EPL]) {
   for (int i = 0; i < EPL; ++i) l[i] *= r;
 }
 
+// Sums of the probabilities, slots per expert and number of the counted
+// tokens among t, t + 1, t + step, t + step + 1, ... below t1, a wave's share.
+template <int EPL>
+__device__ __forceinline__ void count_rows(const RowArgs &a, int t, int t1, int step, float (&l)[kPair][EPL],
+                                           float (&sum)[EPL], int32_t (&cnt)[EPL], int32_t &n) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
+  for (; t < t1; t += step) {
+    int slot[kPair];  // slot j in lane j
+#pragma unroll
+    for (int q = 0; q < kPair; ++q) slot[q] = a.idx[int64_t(min(t + q, t1 - 1)) * a.K + min(lane, a.K - 1)];
+    load_rows<EPL>(a, t, t1, l);
+#pragma unroll
+    for (int q = 0; q < kPair; ++q) {
+      if (t + q >= t1 || (a.tokens.mask && !a.tokens.mask[t + q])) continue;
+      softmax_row<EPL>(l[q]);
+      ++n;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) sum[i] += l[q][i];
+      for (int j = 0; j < a.K; ++j) {
+        const int e = read_lane_i(slot[q], j);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) cnt[i] += e == lane + kWave * i;
+      }
+    }
+  }
+}
+
 // Forward: a workgroup takes a chunk of consecutive tokens and leaves, for
 // every sequence among them, the sums of its counted tokens' probabilities
 // and the counts of their slots, at place chunk number + sequence number
@@ -525,28 +576,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
     const int t1 = a.tokens.off ? max(min(a.tokens.off[b + 1], hi), t0 + 1) : hi;
     float sum[EPL];
     int32_t cnt[EPL], n = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
-    for (int t = t0 + kPair * wave; t < t1; t += kPair * kRowWaves) {
-      int slot[kPair];  // slot j in lane j
-#pragma unroll
-      for (int q = 0; q < kPair; ++q)
-        slot[q] = a.idx[int64_t(min(t + q, t1 - 1)) * a.K + min(lane, a.K - 1)];
-      load_rows<EPL>(a, t, t1, l);
-#pragma unroll
-      for (int q = 0; q < kPair; ++q) {
-        if (t + q >= t1 || (a.tokens.mask && !a.tokens.mask[t + q])) continue;
-        softmax_row<EPL>(l[q]);
-        ++n;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) sum[i] += l[q][i];
-        for (int j = 0; j < a.K; ++j) {
-          const int e = read_lane_i(slot[q], j);
-#pragma unroll
-          for (int i = 0; i < EPL; ++i) cnt[i] += e == lane + kWave * i;
-        }
-      }
-    }
+    count_rows<EPL>(a, t0 + kPair * wave, t1, kPair * kRowWaves, l, sum, cnt, n);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) ps[wave][lane + kWave * i] = sum[i], cs[wave][lane + kWave * i] = cnt[i];
     if (lane == 0) ns[wave] = n;
@@ -635,10 +665,9 @@ __global__ __launch_bounds__(kWave) void balance_loss_kernel(FinishArgs a, int b
   if (lane_id() == 0) a.loss[0] = f > 0.f ? s / f : 0.f;
 }
 
-// Backward of the rows: dl of a chunk of tokens, and their sum.
+// Backward of the rows: dl of a chunk of tokens.
 template <int EPL>
 __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
-  __shared__ float ds[kRowWaves][EPL * kWave];
   const int c0 = int(blockIdx.x) * a.chunk, c1 = min(c0 + a.chunk, a.tokens.T);
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int lo, hi;
@@ -647,10 +676,10 @@ __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
   for (int b = lane; b < a.tokens.n; b += kWave) filled += a.seq_tokens[b] > 0;
   const float nf = wave_sum(float(filled));
   const float up = a.dloss ? a.dloss[0] : 1.0f;
-  float db[EPL], gb[EPL];  // sum of dl; d loss / d p of sequence `of`
+  float gb[EPL];  // d loss / d p of sequence `of`
   int of = -1;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) db[i] = 0.f, gb[i] = 0.f;
+  for (int i = 0; i < EPL; ++i) gb[i] = 0.f;
   for (int t = c0 + kPair * wave; t < c1; t += kPair * kRowWaves) {
     float l[kPair][EPL], dws[kPair], lsel[kPair];
     int slots[kPair];  // slot j in lane j
@@ -731,42 +760,86 @@ __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
           for (int c = 0; c < kPieces; ++c)
             a.dl[(int64_t(c) * a.tokens.T + t + q) * a.ld + e] = uint16_t(w[c]);
         }
-        db[i] += d[i];
       }
     }
   }
-  if (a.dbias) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) ds[wave][lane + kWave * i] = db[i];
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads)
-      a.dbias[int64_t(blockIdx.x) * a.E + e] = ((ds[0][e] + ds[1][e]) + ds[2][e]) + ds[3][e];
+}
+
+// Partial sums of dW and of dbias, added in their order: p holds [parts]
+// records of nw and then nb values, either of which may be unwanted.
+__global__ __launch_bounds__(kThreads) void sum_parts_kernel(const float *p, int parts, int64_t nw, int nb, float *dw,
+                                                             float *db) {
+  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= nw + nb) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int z = 0; z < parts; ++z) s += p[int64_t(z) * (nw + nb) + i];
+  if (i < nw) {
+    if (dw) dw[i] = s;
+  } else if (db) {
+    db[i - nw] = s;
   }
 }
 
-// out[i] = sum over `parts` of p[part * n + i], in order.
-__global__ __launch_bounds__(kThreads) void sum_parts_kernel(const float *p, int parts, int64_t n, float *out) {
-  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.f;
-#pragma unroll 8
-  for (int z = 0; z < parts; ++z) s += p[int64_t(z) * n + i];
-  out[i] = s;
-}
-
-// out[e] = sum over chunks of p[chunk][E], 64 experts per workgroup.
-__global__ __launch_bounds__(kFinishThreads) void sum_chunks_kernel(const float *p, int chunks, int E, float *out) {
-  __shared__ float ps[kFinishRows][kWave];
-  const int lane = lane_id(), row = int(threadIdx.x) / kWave, e = blockIdx.x * kWave + lane;
-  float s = 0.f;
-#pragma unroll 8
-  for (int c = row; c < chunks; c += kFinishRows) s += p[int64_t(c) * E + min(e, E - 1)];
-  ps[row][lane] = s;
-  __syncthreads();
-  if (row) return;
+// The whole reduction of a small call in one workgroup: rows, sums over each
+// sequence's tokens and the loss, instead of three launches that cost more
+// than their work.
+constexpr int kSmallWaves = 8, kSmallTokens = 32, kSmallSeqs = 8;
+template <int EPL>
+__global__ __launch_bounds__(kSmallWaves *kWave) void balance_small_kernel(RowArgs a, FinishArgs f) {
+  __shared__ float ps[kSmallWaves][EPL * kWave], ls[kSmallWaves];
+  __shared__ int32_t cs[kSmallWaves][EPL * kWave], ns[kSmallWaves];
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int T = a.tokens.T;
+  int lo, hi;
+  token_range(a.tokens, lo, hi);
+  float l[kPair][EPL];
+  if (a.parts) {  // tokens of no sequence: their logits alone
+    for (int t = kPair * wave; t < lo; t += kPair * kSmallWaves) load_rows<EPL>(a, t, lo, l);
+    for (int t = hi + kPair * wave; t < T; t += kPair * kSmallWaves) load_rows<EPL>(a, t, T, l);
+  }
+  float loss = 0.f;
+  int filled = 0;
+  for (int b = 0; b < a.tokens.n; ++b) {
+    int t0 = lo, t1 = hi;
+    if (a.tokens.off) {
+      t0 = min(max(a.tokens.off[b], 0), T);
+      t1 = min(max(a.tokens.off[b + 1], t0), T);
+    }
+    float sum[EPL];
+    int32_t cnt[EPL], n = 0;
+    count_rows<EPL>(a, t0 + kPair * wave, t1, kPair * kSmallWaves, l, sum, cnt, n);
 #pragma unroll
-  for (int i = 1; i < kFinishRows; ++i) s += ps[i][lane];
-  if (e < E) out[e] = s;
+    for (int i = 0; i < EPL; ++i) ps[wave][lane + kWave * i] = sum[i], cs[wave][lane + kWave * i] = cnt[i];
+    if (lane == 0) ns[wave] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; ++w) n += ns[w];
+    const float weight = n ? float(a.E) / (float(a.K) * float(n)) : 0.f;
+    for (int e = threadIdx.x; e < a.E; e += kSmallWaves * kWave) {
+      float p = 0.f;
+      int32_t c = 0;
+#pragma unroll
+      for (int w = 0; w < kSmallWaves; ++w) p += ps[w][e], c += cs[w][e];
+      const float m = n ? p / float(n) : 0.f;
+      f.mean[int64_t(b) * a.E + e] = m;
+      f.counts[int64_t(b) * a.E + e] = c;
+      loss += weight * float(c) * m;
+    }
+    if (threadIdx.x == 0) f.seq_tokens[b] = n;
+    filled += n > 0;
+    __syncthreads();
+  }
+  loss = wave_sum(loss);
+  if (lane == 0) ls[wave] = loss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; ++w) s += ls[w];
+    f.loss[0] = filled ? s / float(filled) : 0.f;
+  }
 }
 
 // Tokens per workgroup of the row kernels: 8 (two for each wave), more where
@@ -790,12 +863,13 @@ int router_parts(const moe_layer_desc *d, int32_t T) {
   return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T, kStep), 1024, 4);
 }
 
+// sums_only: bsum is wanted without the product (the first row of tiles makes it).
 template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK>
-void launch_gemm(GemmArgs g, int parts, hipStream_t s) {
+void launch_gemm(GemmArgs g, int parts, hipStream_t s, bool sums_only = false) {
   const int steps = (g.K + kStep - 1) / kStep;
   g.per = (steps + parts - 1) / parts;
-  g.part = int64_t(g.a.rows) * g.b.rows;
-  const dim3 grid(unsigned(tiles_of(g.b.rows)), unsigned(tiles_of(g.a.rows)), unsigned(parts));
+  if (!g.part) g.part = int64_t(g.a.rows) * g.b.rows;
+  const dim3 grid(unsigned(tiles_of(g.b.rows)), sums_only ? 1u : unsigned(tiles_of(g.a.rows)), unsigned(parts));
   if constexpr (DTB == kDtPieces) {
     launch((split_gemm_kernel<DTA, KCA, DTB, KCB, NATIVE, MASK, true>), grid, dim3(kThreads), 0, s, g);
   } else {
@@ -852,8 +926,7 @@ BalanceWorkspace balance_workspace_layout(const moe_layer_desc *d, int32_t T, in
   const int zw = router_parts(d, T);
   b.ld = int((E + 7) / 8 * 8);
   b.dl = take(size_t(kPieces) * T * b.ld * 2);
-  b.dwp = take(zw > 1 ? size_t(zw) * D * E * 4 : 0);
-  b.dbp = take(size_t(chunks_of(T)) * E * 4);
+  b.dwp = take(zw > 1 ? size_t(zw) * (D + 1) * E * 4 : 0);
   b.total = std::max(std::max(fwd, o), size_t(256));
   return b;
 }
@@ -883,6 +956,16 @@ void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, cons
     r.parts = z > 1 ? at<float>(ws, L.parts) : nullptr, r.z = z, r.bias = bias;
     r.logits = logits, r.idx = topk_idx;
     r.psum = at<float>(ws, L.psum), r.count = at<int32_t>(ws, L.count), r.ntok = at<int32_t>(ws, L.ntok);
+    if (T <= kSmallTokens && n_seqs <= kSmallSeqs && E <= 512) {
+      FinishArgs f{};
+      f.counts = counts, f.seq_tokens = seq_tokens, f.mean = mean, f.loss = loss;
+      by_experts(E, [&](auto n) {
+        constexpr int EPL = decltype(n)::value;
+        if constexpr (EPL <= 8)
+          launch((balance_small_kernel<EPL>), dim3(1), dim3(kSmallWaves * kWave), 0, s, r, f);
+      });
+      return;
+    }
     by_experts(E, [&](auto n) {
       launch((balance_rows_kernel<decltype(n)::value>), dim3(chunks_of(T)), dim3(kThreads), 0, s, r);
     });
@@ -909,7 +992,7 @@ void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, 
     r.tokens = tk, r.E = E, r.K = d->top_k, r.chunk = chunk_tokens(T);
     r.logits = const_cast<float *>(logits), r.idx = topk_idx;
     r.counts = counts, r.seq_tokens = seq_tokens, r.dloss = dloss, r.dtopk = dtopk_w, r.renorm = d->renormalize;
-    r.dl = at<uint16_t>(ws, L.dl), r.ld = L.ld, r.dbias = dbias ? at<float>(ws, L.dbp) : nullptr;
+    r.dl = at<uint16_t>(ws, L.dl), r.ld = L.ld;
     by_experts(E, [&](auto n) {
       launch((balance_dlogits_kernel<decltype(n)::value>), dim3(chunks_of(T)), dim3(kThreads), 0, s, r);
     });
@@ -924,26 +1007,25 @@ void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, 
       });
     }
   }
-  if (dw) {
+  if (dw || dbias) {
     const int z = router_parts(d, T);
+    const int64_t nw = int64_t(D) * E;
+    float *const parts = at<float>(ws, L.dwp);
     GemmArgs g{};
     g.a = x_operand(d, T, x, false);
     g.b = dl;
     g.b.rows = E;
-    g.K = T, g.out = z > 1 ? at<float>(ws, L.dwp) : dw;
-    g.tokens = tk;
+    g.K = T, g.tokens = tk;
+    g.out = z > 1 ? parts : dw;
+    g.bsum = z > 1 ? parts + nw : dbias;
+    g.part = g.bpart = nw + E;
     by_dtype(d->act_dtype, [&](auto dt) {
-      launch_gemm<decltype(dt)::value, false, kDtPieces, false, false, true>(g, z, s);
+      launch_gemm<decltype(dt)::value, false, kDtPieces, false, false, true>(g, z, s, !dw);
     });
-    if (z > 1) {
-      const int64_t n = int64_t(D) * E;
-      launch(sum_parts_kernel, dim3(unsigned((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
-             static_cast<const float *>(g.out), z, n, dw);
-    }
+    if (z > 1)
+      launch(sum_parts_kernel, dim3(unsigned((nw + E + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
+             static_cast<const float *>(parts), z, nw, E, dw, dbias);
   }
-  if (dbias)
-    launch(sum_chunks_kernel, dim3((E + kWave - 1) / kWave), dim3(kFinishThreads), 0, s,
-           static_cast<const float *>(at<float>(ws, L.dbp)), T > 0 ? chunks_of(T) : 0, E, dbias);
 }
 
 }  // namespace moe

@@ -81,15 +81,12 @@ __device__ __forceinline__ i32x8 tile_operand(const uint8_t *lds) {
 }
 
 // What a projection writes: the product, or the gated unit of two of them
-// (as e4m3 codes per 128 columns from the tile kernel, as fp32 from the
+// (as e4m3 codes per 128 columns from the tile kernel, as fp32 rows from the
 // decode kernel).
 constexpr int kPlain = 0, kGated = 1;
-// Activations of the decode kernel: codes with scales, or values that it
-// quantises itself (their block maxima are four lanes' work).
-constexpr int kSrcCodes = 3;  // else a moe_dtype
 
 struct Fp8Args {
-  const void *a;             // codes [a_rows][K], or values [a_rows][K] (decode kernel)
+  const void *a;             // codes [a_rows][K]
   const float *as;           // [blocks][a_rows]
   int64_t a_rows;
   const int32_t *row_map;    // null: row p is p
@@ -667,14 +664,12 @@ __global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
 }
 
 // The decode kernel: 16 token rows by WN weight tiles per wave; KW of the
-// four waves split the reduction, the others take further columns.  SRC:
-// codes, or the type of the values that it quantises.
-template <int KW, int WN, int MODE, int SRC>
+// four waves split the reduction, the others take further columns.
+template <int KW, int WN, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
   constexpr int NTH = MODE == kGated ? WN / 2 : WN;
   constexpr int COLS = (kNW / KW) * NTH * 16;
-  constexpr int XB = SRC == kSrcCodes ? 1 : SRC == kDtF32 ? 4 : 2;  // bytes per activation
-  constexpr int DEPTH = XB == 4 ? 3 : 4;  // blocks in flight per wave
+  constexpr int DEPTH = 4;  // blocks in flight per wave
   __shared__ __align__(16) uint8_t turn[kNW][WN][kTileBytes];
   __shared__ float part[KW > 1 ? kNW : 1][KW > 1 ? WN * 4 : 1][kWave];
 
@@ -704,11 +699,11 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
   const int r = lr < tile.rows ? source_row(a, tile.row0 + lr) : -1;
   const bool rok = r >= 0;
   // (rows past the tile read row 0, which the others of their kind share)
-  const char *xp = static_cast<const char *>(a.a) + int64_t(max(r, 0)) * K * XB;
-  const float *sxp = SRC == kSrcCodes ? a.as + max(r, 0) : nullptr;
+  const uint8_t *xp = static_cast<const uint8_t *>(a.a) + int64_t(max(r, 0)) * K;
+  const float *sxp = a.as + max(r, 0);
 
   WeightTile wq[DEPTH][WN];
-  uint4 xq[DEPTH][2][XB];
+  uint4 xq[DEPTH][2];
   float sq[DEPTH][WN], sx[DEPTH];
   auto load = [&](int s, int d) {
     const int k0 = s * kFp8Block;
@@ -719,10 +714,8 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int u = 0; u < XB; ++u)
-        xq[d][h][u] = reinterpret_cast<const uint4 *>(xp + int64_t(min(k0 + 64 * h + lg * 16, K - 16)) * XB)[u];
-    if constexpr (SRC == kSrcCodes) sx[d] = sxp[int64_t(s) * a.a_rows];
+      xq[d][h] = *reinterpret_cast<const uint4 *>(xp + min(k0 + 64 * h + lg * 16, K - 16));
+    sx[d] = sxp[int64_t(s) * a.a_rows];
   };
   fp8_acc acc[WN];
 #pragma unroll
@@ -730,37 +723,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
 
   auto use = [&](int s, int d) {
     const int k0 = s * kFp8Block;
-    const bool ok[2] = {k0 + lg * 16 < K, k0 + 64 + lg * 16 < K};
-    i32x8 x;
-    if constexpr (SRC == kSrcCodes) {
-      x = join8(keep(xq[d][0][0], ok[0] && rok), keep(xq[d][1][0], ok[1] && rok));
-    } else {
-      float v[2][16], mx = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int u = 0; u < XB; ++u) {
-          const uint4 f = keep(xq[d][h][u], ok[h] && rok);
-          const uint32_t g[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (SRC == kDtF32) v[h][4 * u + j] = __uint_as_float(g[j]);
-            else v[h][8 * u + 2 * j] = half_lo<SRC>(g[j]), v[h][8 * u + 2 * j + 1] = half_hi<SRC>(g[j]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[h][i]));
-      }
-      mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
-      mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-      const Fp8Quant q(mx);
-      sx[d] = q.scale;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float *u = &v[j / 4][4 * (j % 4)];
-        x[j] = int(fp8_pack4(q(u[0]), q(u[1]), q(u[2]), q(u[3])));
-      }
-    }
+    const i32x8 x = join8(keep(xq[d][0], rok && k0 + lg * 16 < K), keep(xq[d][1], rok && k0 + 64 + lg * 16 < K));
     const Fp8Operand<true> xo(x);
 #pragma unroll
     for (int nt = 0; nt < WN; ++nt) wq[d][nt].put(turn[wave][nt], K, k0);
@@ -844,11 +807,11 @@ void launch_huge(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   launch(fp8_huge_kernel, dim3(unsigned(tiles * nbx)), dim3(kHugeThreads), 0, s, a);
 }
 
-template <int KW, int WN, int MODE, int SRC>
+template <int KW, int WN, int MODE>
 void launch_decode_one(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   constexpr int COLS = (kNW / KW) * (MODE == kGated ? WN / 2 : WN) * 16;
   const int64_t nbx = (a.N + COLS - 1) / COLS;
-  launch((fp8_decode_kernel<KW, WN, MODE, SRC>), dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
+  launch((fp8_decode_kernel<KW, WN, MODE>), dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
 }
 
 // Waves that split the reduction of the decode kernel.
@@ -859,12 +822,12 @@ int decode_split(int K) {
 // Output columns per workgroup of the decode kernel.
 int decode_cols(int K, bool gated) { return kNW / decode_split(K) * (gated ? 1 : 2) * 16; }
 
-template <int MODE, int SRC>
+template <int MODE>
 void launch_decode(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   const int kw = decode_split(a.K);
-  if (kw == 4) launch_decode_one<4, 2, MODE, SRC>(a, tiles, s);
-  else if (kw == 2) launch_decode_one<2, 2, MODE, SRC>(a, tiles, s);
-  else launch_decode_one<1, 2, MODE, SRC>(a, tiles, s);
+  if (kw == 4) launch_decode_one<4, 2, MODE>(a, tiles, s);
+  else if (kw == 2) launch_decode_one<2, 2, MODE>(a, tiles, s);
+  else launch_decode_one<1, 2, MODE>(a, tiles, s);
 }
 
 }  // namespace
@@ -918,15 +881,18 @@ void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, in
   const bool exact = out_dtype == MOE_DT_F32;
   const int bm = fp8_tile_rows(rows, N, K, n_experts, exact);
   const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
-  if (bm == 16) launch_decode<kPlain, kSrcCodes>(g, tiles, s);
+  if (bm == 16) launch_decode<kPlain>(g, tiles, s);
   else if (exact) launch_tile<kPlain, true>(g, tiles, s);
   else if (bm == 64) launch_tile<kPlain, false>(g, tiles, s);
   else if (bm == 128) launch_wide(g, tiles, s);
   else launch_huge(g, tiles, s);
 }
 
-// Workspace of the expert FFN: x codes and scales (tile kernels), h as codes
-// and scales or as fp32.
+// The codes of the decode tiles' h, behind its fp32 rows (h_bytes counts them).
+static uint8_t *codes_of_h(void *h, int64_t rows, int F) { return static_cast<uint8_t *>(h) + rows * F * 4; }
+
+// Workspace of the expert FFN: x codes and scales, h as codes and scales and
+// (decode tiles) as fp32 rows.
 void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, const int32_t *row_map,
                            const moe_weights *w, const int32_t *counters, const PlanItem *tiles,
                            const FfnScratch &sc, float *y_sorted, void *stream, StageMarker *mk) {
@@ -950,24 +916,29 @@ void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, co
   n.E = M, n.tiles = tiles, n.counters = counters;
   n.a = sc.h, n.a_rows = R;
   n.out = y_sorted, n.out_dtype = MOE_DT_F32;
-  if (bm == 16) {  // both projections quantise their own rows; h is fp32
-    g.a = x;
-    g.out_dtype = MOE_DT_F32;
-    if (d->act_dtype == MOE_DT_BF16) launch_decode<kGated, kDtBF16>(g, max_tiles, s);
-    else if (d->act_dtype == MOE_DT_F16) launch_decode<kGated, kDtF16>(g, max_tiles, s);
-    else launch_decode<kGated, kDtF32>(g, max_tiles, s);
-    if (mk) mk->mark("gateup_fp8");
-    launch_decode<kPlain, kDtF32>(n, max_tiles, s);
-    if (mk) mk->mark("down_fp8");
-    return;
-  }
   uint8_t *xq = static_cast<uint8_t *>(sc.x16);
   float *xs = reinterpret_cast<float *>(sc.xg);
   float *hs = reinterpret_cast<float *>(sc.hsh);
+  // x is quantised once, not by every workgroup for its own rows: that saved
+  // two launches on the decode tiles but repeated the work so often that it
+  // lost even at one token (21.6 against 20.0 us for 128 experts of 2048 x 768,
+  // top 8; 32 tokens 136 against 101 us, 256 tokens 236 against 152 us).
   launch_fp8_rows(x, d->act_dtype, T, D, xq, xs, stream);
   if (mk) mk->mark("x_fp8");
   g.a = xq, g.as = xs, g.hs = hs;
   n.as = hs;
+  if (bm == 16) {  // a workgroup's 16 columns do not make a block of h: fp32 rows first
+    g.out_dtype = MOE_DT_F32;
+    launch_decode<kGated>(g, max_tiles, s);
+    if (mk) mk->mark("gateup_fp8");
+    uint8_t *hq = codes_of_h(sc.h, R, F);
+    launch_fp8_rows(sc.h, MOE_DT_F32, R, F, hq, hs, stream);
+    if (mk) mk->mark("h_fp8");
+    n.a = hq;
+    launch_decode<kPlain>(n, max_tiles, s);
+    if (mk) mk->mark("down_fp8");
+    return;
+  }
   launch_tile<kGated, true>(g, max_tiles, s);
   if (mk) mk->mark("gateup_fp8");
   launch_tile<kPlain, true>(n, max_tiles, s);

@@ -109,9 +109,9 @@ inline bool affine(const moe_layer_desc *d) {
   return d->w_format == MOE_WF_AFFINE_Q4 || d->w_format == MOE_WF_AFFINE_Q8;
 }
 // Bytes per element of the GLU intermediate h (16-bit for bf16 and fp16
-// layers; fp32, or codes in the same place, for fp8 layers).
+// layers; fp32 and a code for fp8 layers).
 inline int64_t h_bytes(const moe_layer_desc *d) {
-  return d->act_dtype == MOE_DT_F32 || d->w_format == MOE_WF_FP8 ? 4 : 2;
+  return d->w_format == MOE_WF_FP8 ? 5 : d->act_dtype == MOE_DT_F32 ? 4 : 2;
 }
 // 8-bit floating point expert weights.
 inline bool fp8(const moe_layer_desc *d) { return d->w_format == MOE_WF_FP8; }
@@ -340,7 +340,7 @@ constexpr int kMaxSeqs = 4096;
 struct BalanceWorkspace {
   size_t parts;                     // forward: [z][T][E] partial logits (z > 1)
   size_t psum, count, ntok, terms;  // records per (chunk of tokens, sequence); loss terms
-  size_t dl, dwp, dbp;              // backward: [3][T][ld] logit gradients, [z][D][E] (z > 1), [chunks][E]
+  size_t dl, dwp;                   // backward: [3][T][ld] logit gradients; [z][D + 1][E] parts of dW, dbias (z > 1)
   int ld;
   size_t total;
 };
