@@ -1452,7 +1452,7 @@ int plan_tile_rows(const moe_layer_desc *d, int32_t T) {
   // Decode-sized groups (T*k/E <= 8 rows per expert on average, the pages'
   // small-group regime) use 16-row tiles; larger groups 64-row tiles.
   const int64_t N = int64_t(T) * d->top_k;
-  if (fp8(d)) return N <= 16LL * d->n_experts ? 16 : 64;  // as for one product (fp8_tile_rows)
+  if (fp8(d)) return N <= 16LL * d->n_experts ? 16 : fp8_small_tile(N, d->n_experts);  // as for one product
   return N <= 8LL * d->n_experts ? 16 : 64;
 }
 

@@ -195,12 +195,13 @@ __device__ __forceinline__ void store4(const Fp8Args &a, int64_t at, const fp8_a
   }
 }
 
-// The 64-row tile.  Weights and rows are requested two blocks ahead of their
-// use, into two sets of registers: with one block in flight a workgroup
-// waited out a memory round trip per block.  EXACT: see Fp8Operand.
-template <int MODE, bool EXACT>
+// The tile of 16 RB token rows (32, 48 or 64).  Weights and rows are requested
+// two blocks ahead of their use, into two sets of registers: with one block
+// in flight a workgroup waited out a memory round trip per block.  EXACT: see
+// Fp8Operand.
+template <int RB, int MODE, bool EXACT>
 __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
-  constexpr int RB = 4, BM = RB * 16;
+  constexpr int BM = RB == 2 ? 32 : 64;             // rows that are staged (zeros past the tile's)
   constexpr int NP = 2;                             // weight tiles that a read of the rows serves
   // rows in LDS: codes, or (EXACT) fp16, turned into it once here instead of
   // by every wave for every weight tile; 16 bytes of padding put the pieces
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
   // one of gate rows, and two of up rows when they start inside a block
   constexpr int NS = MODE == kGated ? 3 : 2;
   constexpr int NSL = kThreads / BM;                // one scale per thread (those past NS repeat the last)
-  static_assert(NS <= NSL, "one scale per thread");
+  static_assert(NS <= NSL && RB * 16 <= BM, "one scale per thread");
   __shared__ __align__(16) uint8_t sa[2][BM][ROW];
   __shared__ __align__(16) uint8_t turn[kNW][kNT][kTileBytes];
   __shared__ float ss[2][NSL][BM];                  // row scale * weight scale
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
   const int nbx = (a.N + COLS - 1) / COLS;
   PlanItem tile;
   int bx;
-  if (!my_work(a, BM, nbx, tile, bx)) return;
+  if (!my_work(a, RB * 16, nbx, tile, bx)) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = lane_id();
   const int lr = lane & 15, lg = lane >> 4;
   const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[np + q][mt][i] = __builtin_fmaf(d[i], sc, acc[np + q][mt][i]);
         }
-        if (EXACT && mt % 2) __builtin_amdgcn_sched_barrier(0);  // (more reads ahead would not fit the registers)
+        if (EXACT && RB == 4 && mt % 2) __builtin_amdgcn_sched_barrier(0);  // (more reads ahead would not fit the registers)
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -791,11 +792,15 @@ int64_t most_tiles(int64_t rows, int experts, int bm) {
   return rows / bm + std::min<int64_t>(rows, experts);
 }
 
+// bm: 32, 48 or 64 rows a tile.
 template <int MODE, bool EXACT>
-void launch_tile(const Fp8Args &a, int64_t tiles, hipStream_t s) {
+void launch_tile(const Fp8Args &a, int bm, int64_t tiles, hipStream_t s) {
   constexpr int COLS = MODE == kGated ? kBN / 2 : kBN;
   const int64_t nbx = (a.N + COLS - 1) / COLS;
-  launch((fp8_tile_kernel<MODE, EXACT>), dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
+  const dim3 grid(unsigned(tiles * nbx));
+  if (bm == 32) launch((fp8_tile_kernel<2, MODE, EXACT>), grid, dim3(kThreads), 0, s, a);
+  else if (bm == 48) launch((fp8_tile_kernel<3, MODE, EXACT>), grid, dim3(kThreads), 0, s, a);
+  else launch((fp8_tile_kernel<4, MODE, EXACT>), grid, dim3(kThreads), 0, s, a);
 }
 void launch_wide(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   const int64_t nbx = (a.N + kBN - 1) / kBN;
@@ -842,10 +847,14 @@ void launch_decode(const Fp8Args &a, int64_t tiles, hipStream_t s) {
 // the GPU at most about once over, or at most 16 rows an expert; 64 while its
 // workgroups fit the GPU at once, or experts would leave a larger tile half
 // empty; 256 from two of its tiles per CU on.
+int fp8_small_tile(int64_t rows, int experts) {
+  return rows <= 26LL * experts ? 32 : rows <= 42LL * experts ? 48 : 64;
+}
 int fp8_tile_rows(int64_t rows, int32_t N, int32_t K, int experts, bool exact) {
   const int64_t t16 = most_tiles(rows, experts, 16), t64 = rows / 64 + experts / 2;
   const int dc = decode_cols(K, false), nbx = (N + kBN - 1) / kBN;
   if (rows <= 16LL * experts || t16 * ((N + dc - 1) / dc) <= 2560) return 16;
+  if (rows <= 42LL * experts) return fp8_small_tile(rows, experts);
   if (exact || rows < 96LL * experts || t64 * nbx <= 640) return 64;
   return rows / kHugeRows * nbx >= 512 && rows >= 1024LL * experts ? 256 : 128;
 }
@@ -882,8 +891,8 @@ void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, in
   const int bm = fp8_tile_rows(rows, N, K, n_experts, exact);
   const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
   if (bm == 16) launch_decode<kPlain>(g, tiles, s);
-  else if (exact) launch_tile<kPlain, true>(g, tiles, s);
-  else if (bm == 64) launch_tile<kPlain, false>(g, tiles, s);
+  else if (exact) launch_tile<kPlain, true>(g, bm, tiles, s);
+  else if (bm <= 64) launch_tile<kPlain, false>(g, bm, tiles, s);
   else if (bm == 128) launch_wide(g, tiles, s);
   else launch_huge(g, tiles, s);
 }
@@ -939,9 +948,9 @@ void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, co
     if (mk) mk->mark("down_fp8");
     return;
   }
-  launch_tile<kGated, true>(g, max_tiles, s);
+  launch_tile<kGated, true>(g, bm, max_tiles, s);
   if (mk) mk->mark("gateup_fp8");
-  launch_tile<kPlain, true>(n, max_tiles, s);
+  launch_tile<kPlain, true>(n, bm, max_tiles, s);
   if (mk) mk->mark("down_fp8");
 }
 

@@ -319,6 +319,7 @@ void launch_fp8_blocks(const void *x, int32_t dtype, int32_t matrices, int32_t r
 // Rows per tile of the grouped product.  exact: fp32 sums of 16-bit products
 // (fp32 results), else the 8-bit instruction.
 int fp8_tile_rows(int64_t rows, int32_t N, int32_t K, int experts, bool exact);
+int fp8_small_tile(int64_t rows, int experts);  // 32, 48 or 64
 // Workgroups of the grids that the grouped product and the fp8 layer launch
 // (at most kMaxGroups: the threads of a grid are counted in 32 bits).
 constexpr int64_t kMaxGroups = (1 << 24) - 1;
