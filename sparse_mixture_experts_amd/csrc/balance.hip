@@ -318,7 +318,11 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
   using SA = Stage<DTA, KCA, NATIVE, true>;
   using SB = Stage<DTB, KCB, NATIVE, VECB>;
   constexpr int PA = SA::P, PB = SB::P, S = 2;
-  __shared__ __align__(16) uint16_t la[PA][kTile * kStep], lb[PB][kTile * kStep];
+  // Two buffers (one barrier a step, a step's elements stored while the last
+  // one's are multiplied) for single pieces; with more, the second one costs
+  // occupancy (8192 tokens, 128 experts, dx: 34 us with one, 39 with two).
+  constexpr int BUF = PA + PB <= 2 ? 2 : 1;
+  __shared__ __align__(16) uint16_t la[BUF][PA][kTile * kStep], lb[BUF][PB][kTile * kStep];
   const int lane = lane_id(), wave = threadIdx.x / kWave, lr = lane & 15, lg = lane >> 4;
   const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
   const int wm = (wave >> 1) * 16 * S, wn = (wave & 1) * 16 * S;
@@ -348,13 +352,13 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
     sa[r].template load<MASK>(g.a, m0, start_of(s), g.K, g.tokens, lo, hi);
     sb[r].template load<MASK>(g.b, n0, start_of(s), g.K, g.tokens, lo, hi);
   };
-  auto step = [&](int s, auto rc) {
+  auto store = [&](int s, auto rc) {  // step s from its registers into its buffer
     constexpr int r = decltype(rc)::value;
-    __syncthreads();
-    sa[r].store(la, start_of(s), s * kStep, g.K);
-    sb[r].store(lb, start_of(s), s * kStep, g.K);
-    __syncthreads();
-    if (s + 2 < s1) load(s + 2, rc);
+    sa[r].store(la[r % BUF], start_of(s), s * kStep, g.K);
+    sb[r].store(lb[r % BUF], start_of(s), s * kStep, g.K);
+  };
+  auto multiply = [&](auto rc) {
+    constexpr int r = decltype(rc)::value % BUF;
 #pragma unroll
     for (int kk = 0; kk < kStep; kk += 32) {
       uint4 fa[PA][S];
@@ -362,12 +366,12 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
       for (int p = 0; p < PA; ++p)
 #pragma unroll
         for (int i = 0; i < S; ++i)
-          fa[p][i] = *reinterpret_cast<const uint4 *>(&la[p][lds_at(wm + i * 16 + lr, kk + lg * 8)]);
+          fa[p][i] = *reinterpret_cast<const uint4 *>(&la[r][p][lds_at(wm + i * 16 + lr, kk + lg * 8)]);
 #pragma unroll
       for (int q = PB - 1; q >= 0; --q)
 #pragma unroll
         for (int j = 0; j < S; ++j) {
-          const uint4 fb = *reinterpret_cast<const uint4 *>(&lb[q][lds_at(wn + j * 16 + lr, kk + lg * 8)]);
+          const uint4 fb = *reinterpret_cast<const uint4 *>(&lb[r][q][lds_at(wn + j * 16 + lr, kk + lg * 8)]);
           if constexpr (MASK && !NATIVE) {
             if (sums)
               accb[j] = mfma_bf16(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, ones), accb[j]);
@@ -388,15 +392,33 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
   };
   using R0 = std::integral_constant<int, 0>;
   using R1 = std::integral_constant<int, 1>;
+  auto step = [&](int s, auto rc, auto next) {
+    if constexpr (BUF == 1) {
+      __syncthreads();
+      store(s, rc);
+      __syncthreads();
+      if (s + 2 < s1) load(s + 2, rc);
+      multiply(rc);
+    } else {  // step s lies in its buffer
+      if (s + 2 < s1) load(s + 2, rc);
+      multiply(rc);
+      if (s + 1 < s1) store(s + 1, next);
+      __syncthreads();
+    }
+  };
   if (s0 < s1) {
     load(s0, R0{});
     load(min(s0 + 1, s1 - 1), R1{});
+    if constexpr (BUF == 2) {
+      store(s0, R0{});
+      __syncthreads();
+    }
     int s = s0;
     for (; s + 1 < s1; s += 2) {
-      step(s, R0{});
-      step(s + 1, R1{});
+      step(s, R0{}, R1{});
+      step(s + 1, R1{}, R0{});
     }
-    if (s < s1) step(s, R0{});
+    if (s < s1) step(s, R0{}, R1{});
   }
   const int N = g.b.rows;
   if (sums && lr == 0) {  // every column of the product holds the same sums
@@ -460,6 +482,7 @@ struct RowArgs {
   float *psum;             // [slots][E]
   int32_t *count;          // [slots][E]
   int32_t *ntok;           // [slots]
+  int32_t *ticket;         // set to 0 for the kernel that follows
   // backward
   const int32_t *counts, *seq_tokens;  // [n][E], [n]
   const float *dloss;
@@ -524,59 +547,41 @@ __device__ __forceinline__ void softmax_row(float (&l)[EPL]) {
   for (int i = 0; i < EPL; ++i) l[i] *= r;
 }
 
-// Sums of the probabilities, slots per expert and number of the counted
-// tokens among t, t + 1, t + step, t + step + 1, ... below t1, a wave's share.
+// One counted token: its probabilities and its slots (slot j in lane j).
 template <int EPL>
-__device__ __forceinline__ void count_rows(const RowArgs &a, int t, int t1, int step, float (&l)[kPair][EPL],
-                                           float (&sum)[EPL], int32_t (&cnt)[EPL], int32_t &n) {
-  const int lane = lane_id();
+__device__ __forceinline__ void count_row(const RowArgs &a, float (&l)[EPL], int slot, float (&sum)[EPL],
+                                          int32_t (&cnt)[EPL], int32_t &n) {
+  softmax_row<EPL>(l);
+  ++n;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
-  for (; t < t1; t += step) {
-    int slot[kPair];  // slot j in lane j
+  for (int i = 0; i < EPL; ++i) sum[i] += l[i];
+  for (int j = 0; j < a.K; ++j) {
+    const int e = read_lane_i(slot, j);
 #pragma unroll
-    for (int q = 0; q < kPair; ++q) slot[q] = a.idx[int64_t(min(t + q, t1 - 1)) * a.K + min(lane, a.K - 1)];
-    load_rows<EPL>(a, t, t1, l);
-#pragma unroll
-    for (int q = 0; q < kPair; ++q) {
-      if (t + q >= t1 || (a.tokens.mask && !a.tokens.mask[t + q])) continue;
-      softmax_row<EPL>(l[q]);
-      ++n;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) sum[i] += l[q][i];
-      for (int j = 0; j < a.K; ++j) {
-        const int e = read_lane_i(slot[q], j);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) cnt[i] += e == lane + kWave * i;
-      }
-    }
+    for (int i = 0; i < EPL; ++i) cnt[i] += e == lane_id() + kWave * i;
   }
 }
 
-// Forward: a workgroup takes a chunk of consecutive tokens and leaves, for
-// every sequence among them, the sums of its counted tokens' probabilities
-// and the counts of their slots, at place chunk number + sequence number
-// (which no other pair shares).
+// Forward: a workgroup takes a chunk of consecutive tokens, 8 at a time, and
+// leaves, for every sequence among them, the sums of its counted tokens'
+// probabilities and the counts of their slots, at place chunk number +
+// sequence number (which no other pair shares).  A wave's two rows are
+// requested before the tokens' sequence is looked up.
 template <int EPL>
 __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
   __shared__ float ps[kRowWaves][EPL * kWave];
   __shared__ int32_t cs[kRowWaves][EPL * kWave], ns[kRowWaves];
   const int c0 = int(blockIdx.x) * a.chunk, c1 = min(c0 + a.chunk, a.tokens.T);
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  int lo, hi;
-  token_range(a.tokens, lo, hi);
-  lo = min(max(lo, c0), c1), hi = max(min(hi, c1), lo);
-  float l[kPair][EPL];
-  if (a.parts) {  // tokens of no sequence: their logits alone
-    for (int t = c0 + kPair * wave; t < lo; t += kPair * kRowWaves) load_rows<EPL>(a, t, lo, l);
-    for (int t = hi + kPair * wave; t < c1; t += kPair * kRowWaves) load_rows<EPL>(a, t, c1, l);
-  }
-  for (int t0 = lo; t0 < hi;) {  // one sequence's tokens t0 .. t1 - 1
-    const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t0));
-    const int t1 = a.tokens.off ? max(min(a.tokens.off[b + 1], hi), t0 + 1) : hi;
-    float sum[EPL];
-    int32_t cnt[EPL], n = 0;
-    count_rows<EPL>(a, t0 + kPair * wave, t1, kPair * kRowWaves, l, sum, cnt, n);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  float sum[EPL];
+  int32_t cnt[EPL], n;
+  auto reset = [&] {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
+    n = 0;
+  };
+  auto flush = [&](int b) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) ps[wave][lane + kWave * i] = sum[i], cs[wave][lane + kWave * i] = cnt[i];
     if (lane == 0) ns[wave] = n;
@@ -592,8 +597,43 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
     }
     if (threadIdx.x == 0) a.ntok[at] = ns[0] + ns[1] + ns[2] + ns[3];
     __syncthreads();
-    t0 = t1;
+    reset();
+  };
+  reset();
+  int b = -1, end = 0;  // the sequence of the tokens at hand, where it ends
+  for (int c = c0; c < c1; c += kPair * kRowWaves) {
+    const int tw = c + kPair * wave;
+    float l[kPair][EPL];
+    int slot[kPair];
+    bool on[kPair];
+#pragma unroll
+    for (int q = 0; q < kPair; ++q) {
+      const int t = min(tw + q, c1 - 1);
+      slot[q] = a.idx[int64_t(t) * a.K + min(lane, a.K - 1)];  // slot j in lane j
+      on[q] = !a.tokens.mask || a.tokens.mask[t];
+    }
+    load_rows<EPL>(a, tw, c1, l);
+    int lo, hi;
+    token_range(a.tokens, lo, hi);
+    int t0 = max(c, lo);
+    const int t2 = min(min(c + kPair * kRowWaves, c1), hi);
+    while (t0 < t2) {  // the part of these tokens that lies in one sequence
+      if (b < 0 || t0 >= end) {
+        const int nb = __builtin_amdgcn_readfirstlane(sequence_of(a.tokens, t0));
+        if (b >= 0 && nb != b) flush(b);
+        b = nb;
+        end = a.tokens.off ? max(a.tokens.off[b + 1], t0 + 1) : hi;
+      }
+      const int t1 = min(t2, end);
+#pragma unroll
+      for (int q = 0; q < kPair; ++q) {
+        if (tw + q < t0 || tw + q >= t1 || !on[q]) continue;
+        count_row<EPL>(a, l[q], slot[q], sum, cnt, n);
+      }
+      t0 = t1;
+    }
   }
+  if (b >= 0) flush(b);
 }
 
 struct FinishArgs {
@@ -604,6 +644,7 @@ struct FinishArgs {
   int32_t *counts, *seq_tokens;
   float *mean;
   float *terms;   // [n][blocks of 64 experts]: sum of count * mean
+  int32_t *ticket;
   float *loss;
 };
 
@@ -611,6 +652,7 @@ constexpr int kFinishThreads = 1024;
 constexpr int kFinishRows = kFinishThreads / kWave;  // records summed side by side (16)
 
 // One sequence and 64 experts: the records of its chunks, 16 side by side.
+// The workgroup that is the last to finish adds up the loss, in a fixed order.
 __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(FinishArgs a) {
   __shared__ float ps[kFinishRows][kWave];
   __shared__ int32_t cs[kFinishRows][kWave], ns[kFinishRows];
@@ -642,27 +684,25 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(FinishAr
     a.mean[int64_t(b) * a.E + e] = m;
     a.counts[int64_t(b) * a.E + e] = c;
   }
-  const float term = wave_sum(e < a.E ? float(c) * m : 0.f);
+  // this workgroup's part of sum_b E / (k n_b) sum_e c_be P_be
+  const float term = wave_sum(e < a.E ? float(c) * m : 0.f) * (n ? float(a.E) / (float(a.K) * float(n)) : 0.f);
+  const int blocks = gridDim.x, total = blocks * gridDim.y;
+  int last = total == 1;
   if (lane == 0) {
-    a.terms[b * gridDim.x + blockIdx.x] = term;
-    if (blockIdx.x == 0) a.seq_tokens[b] = n;
-    if (gridDim.x * gridDim.y == 1) a.loss[0] = n ? term * (float(a.E) / (float(a.K) * float(n))) : 0.f;
+    if (blockIdx.x == 0) __hip_atomic_store(a.seq_tokens + b, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(a.terms + b * blocks + blockIdx.x, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (total > 1)
+      last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
   }
-}
-
-// The loss from the sequences' terms, one wave.
-__global__ __launch_bounds__(kWave) void balance_loss_kernel(FinishArgs a, int blocks) {
-  float s = 0.f;
-  int filled = 0;
-  for (int b = lane_id(); b < a.tokens.n; b += kWave) {
-    const int n = a.seq_tokens[b];
-    float v = 0.f;
-    for (int i = 0; i < blocks; ++i) v += a.terms[b * blocks + i];
-    if (n) s += v * (float(a.E) / (float(a.K) * float(n))), ++filled;
-  }
+  if (!__builtin_amdgcn_readfirstlane(last)) return;
+  float s = 0.f, f = 0.f;
+  for (int i = lane; i < total; i += kWave)
+    s += __hip_atomic_load(a.terms + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = lane; i < int(gridDim.y); i += kWave)
+    f += __hip_atomic_load(a.seq_tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0 ? 1.f : 0.f;
   s = wave_sum(s);
-  const float f = wave_sum(float(filled));
-  if (lane_id() == 0) a.loss[0] = f > 0.f ? s / f : 0.f;
+  f = wave_sum(f);
+  if (lane == 0) a.loss[0] = f > 0.f ? s / f : 0.f;
 }
 
 // Backward of the rows: dl of a chunk of tokens.
@@ -808,7 +848,17 @@ __global__ __launch_bounds__(kSmallWaves *kWave) void balance_small_kernel(RowAr
     }
     float sum[EPL];
     int32_t cnt[EPL], n = 0;
-    count_rows<EPL>(a, t0 + kPair * wave, t1, kPair * kSmallWaves, l, sum, cnt, n);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
+    for (int t = t0 + kPair * wave; t < t1; t += kPair * kSmallWaves) {
+      int slot[kPair];
+#pragma unroll
+      for (int q = 0; q < kPair; ++q) slot[q] = a.idx[int64_t(min(t + q, t1 - 1)) * a.K + min(lane, a.K - 1)];
+      load_rows<EPL>(a, t, t1, l);
+#pragma unroll
+      for (int q = 0; q < kPair; ++q)
+        if (t + q < t1 && (!a.tokens.mask || a.tokens.mask[t + q])) count_row<EPL>(a, l[q], slot[q], sum, cnt, n);
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) ps[wave][lane + kWave * i] = sum[i], cs[wave][lane + kWave * i] = cnt[i];
     if (lane == 0) ns[wave] = n;
@@ -860,7 +910,7 @@ int logit_parts(const moe_layer_desc *d, int32_t T) {
   return parts_of(int64_t(tiles_of(T)) * tiles_of(d->n_experts), tiles_of(d->d_model, kStep), 512, 2);
 }
 int router_parts(const moe_layer_desc *d, int32_t T) {
-  return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T, kStep), 1024, 4);
+  return parts_of(int64_t(tiles_of(d->d_model)) * tiles_of(d->n_experts), tiles_of(T, kStep), 512, 2);
 }
 
 // sums_only: bsum is wanted without the product (the first row of tiles makes it).
@@ -921,6 +971,7 @@ BalanceWorkspace balance_workspace_layout(const moe_layer_desc *d, int32_t T, in
   b.count = take(slots * E * 4);
   b.ntok = take(slots * 4);
   b.terms = take(size_t(n_seqs) * ((E + kWave - 1) / kWave) * 4);
+  b.ticket = take(4);
   const size_t fwd = o;
   o = 0;
   const int zw = router_parts(d, T);
@@ -939,8 +990,8 @@ void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, cons
   const int E = d->n_experts, D = d->d_model;
   const BalanceWorkspace L = balance_workspace_layout(d, T, n_seqs);
   const Tokens tk{mask, seq_off, n_seqs, T};
+  const int z = T > 0 ? logit_parts(d, T) : 1;
   if (T > 0) {
-    const int z = logit_parts(d, T);
     GemmArgs g{};
     g.a = x_operand(d, T, x, true);
     g.b = Operand{w_router, E, E, E % 4 == 0};
@@ -951,30 +1002,30 @@ void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, cons
       constexpr int DT = decltype(dt)::value;
       launch_gemm<DT, true, DT, false, DT == kDtF16, false>(g, z, s);
     });
-    RowArgs r{};
-    r.tokens = tk, r.E = E, r.K = d->top_k, r.chunk = chunk_tokens(T);
-    r.parts = z > 1 ? at<float>(ws, L.parts) : nullptr, r.z = z, r.bias = bias;
-    r.logits = logits, r.idx = topk_idx;
-    r.psum = at<float>(ws, L.psum), r.count = at<int32_t>(ws, L.count), r.ntok = at<int32_t>(ws, L.ntok);
-    if (T <= kSmallTokens && n_seqs <= kSmallSeqs && E <= 512) {
-      FinishArgs f{};
-      f.counts = counts, f.seq_tokens = seq_tokens, f.mean = mean, f.loss = loss;
-      by_experts(E, [&](auto n) {
-        constexpr int EPL = decltype(n)::value;
-        if constexpr (EPL <= 8)
-          launch((balance_small_kernel<EPL>), dim3(1), dim3(kSmallWaves * kWave), 0, s, r, f);
-      });
-      return;
-    }
-    by_experts(E, [&](auto n) {
-      launch((balance_rows_kernel<decltype(n)::value>), dim3(chunks_of(T)), dim3(kThreads), 0, s, r);
-    });
   }
+  RowArgs r{};
+  r.tokens = tk, r.E = E, r.K = d->top_k, r.chunk = chunk_tokens(T);
+  r.parts = z > 1 ? at<float>(ws, L.parts) : nullptr, r.z = z, r.bias = bias;
+  r.logits = logits, r.idx = topk_idx;
+  r.psum = at<float>(ws, L.psum), r.count = at<int32_t>(ws, L.count), r.ntok = at<int32_t>(ws, L.ntok);
+  r.ticket = at<int32_t>(ws, L.ticket);
+  if (T <= kSmallTokens && n_seqs <= kSmallSeqs && E <= 512) {
+    FinishArgs f{};
+    f.counts = counts, f.seq_tokens = seq_tokens, f.mean = mean, f.loss = loss;
+    by_experts(E, [&](auto n) {
+      constexpr int EPL = decltype(n)::value;
+      if constexpr (EPL <= 8)
+        launch((balance_small_kernel<EPL>), dim3(1), dim3(kSmallWaves * kWave), 0, s, r, f);
+    });
+    return;
+  }
+  by_experts(E, [&](auto n) {  // (without tokens: for the ticket alone)
+    launch((balance_rows_kernel<decltype(n)::value>), dim3(std::max(1, chunks_of(T))), dim3(kThreads), 0, s, r);
+  });
   FinishArgs f{tk, E, d->top_k, chunk_tokens(T), at<float>(ws, L.psum), at<int32_t>(ws, L.count), at<int32_t>(ws, L.ntok),
-               counts, seq_tokens, mean, at<float>(ws, L.terms), loss};
+               counts, seq_tokens, mean, at<float>(ws, L.terms), at<int32_t>(ws, L.ticket), loss};
   const int blocks = (E + kWave - 1) / kWave;
   launch(balance_finish_kernel, dim3(blocks, n_seqs), dim3(kFinishThreads), 0, s, f);
-  if (blocks * n_seqs > 1) launch(balance_loss_kernel, dim3(1), dim3(kWave), 0, s, f, blocks);
 }
 
 void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, const void *w_router,

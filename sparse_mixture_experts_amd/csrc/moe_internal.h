@@ -340,7 +340,8 @@ void launch_expert_ffn_fp8(const moe_layer_desc *d, int32_t T, const void *x, co
 constexpr int kMaxSeqs = 4096;
 struct BalanceWorkspace {
   size_t parts;                     // forward: [z][T][E] partial logits (z > 1)
-  size_t psum, count, ntok, terms;  // records per (chunk of tokens, sequence); loss terms
+  size_t psum, count, ntok;         // forward: records per (chunk of tokens, sequence)
+  size_t terms, ticket;             // forward: loss terms; workgroups that have finished
   size_t dl, dwp;                   // backward: [3][T][ld] logit gradients; [z][D + 1][E] parts of dW, dbias (z > 1)
   int ld;
   size_t total;

@@ -30,6 +30,9 @@ CASES = [
     (70, 2048, 512, 10, "bf16", [33, 37], True, True, True),
     (40, 128, 1024, 8, "f32", [20, 20], False, False, False),
     (2100, 64, 24, 2, "bf16", [700] * 3, True, False, True),           # many chunks: split sums over tokens
+    (31, 200, 400, 7, "f16", [3, 0, 20, 4], True, True, True),         # reduced in one workgroup
+    (900, 72, 130, 3, "f32", [1] * 37 + [400, 0, 463], False, True, True),
+    (8300, 64, 16, 2, "f16", [4000, 100, 4200], True, False, False),   # 32 tokens a workgroup
 ]
 IDS = [f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-{c[4]}" for c in CASES]
 
@@ -289,6 +292,9 @@ def test_nothing_counts():
     s["mask"][:] = 0
     cases = [s, make(12, 64, 9, 2, "f32", [0, 0, 0], False, False, False), make(0, 64, 9, 2, "f16", None, False, False, True)]
     cases.append(make(0, 64, 9, 2, "bf16", [0, 0], True, True, True))
+    cases.append(make(0, 64, 9, 2, "bf16", [0] * 20, False, False, True))
+    cases.append(make(0, 64, 600, 2, "bf16", None, False, False, True))
+    cases.append(make(40, 64, 9, 2, "bf16", [0] * 11, False, False, True))
     for q in cases:
         o = forward(q)
         assert float(o["loss"]) == 0 and (o["counts"] == 0).all() and (o["tokens"] == 0).all() and (o["mean"] == 0).all()
