@@ -151,7 +151,7 @@ struct Stage {
         constexpr int C = DT == kDtF32 ? 4 : 8;  // elements of a 16-byte piece
 #pragma unroll
         for (int u = 0; u < 16 / C; ++u) {
-          const int64_t at = row + min(c + C * u, K - C);  // (K < 64: start is 0)
+          const int64_t at = row + min(c + C * u, K - C - start);
           const uint4 q = DT == kDtF32 ? *reinterpret_cast<const uint4 *>(pf + at)
                                        : *reinterpret_cast<const uint4 *>(ph + at);
           w[4 * u] = q.x, w[4 * u + 1] = q.y, w[4 * u + 2] = q.z, w[4 * u + 3] = q.w;

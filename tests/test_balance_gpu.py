@@ -33,6 +33,8 @@ CASES = [
     (31, 200, 400, 7, "f16", [3, 0, 20, 4], True, True, True),         # reduced in one workgroup
     (900, 72, 130, 3, "f32", [1] * 37 + [400, 0, 463], False, True, True),
     (8300, 64, 16, 2, "f16", [4000, 100, 4200], True, False, False),   # 32 tokens a workgroup
+    (90, 72, 68, 4, "f32", None, False, True, True),                   # router rows of 4 beyond a step of 64 and a multiple of 8
+    (33, 40, 132, 3, "f32", [20, 13], True, False, False),
 ]
 IDS = [f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-{c[4]}" for c in CASES]
 
