@@ -464,7 +464,8 @@ int moe_fp8_quantize(int32_t n_matrices, int32_t rows, int32_t cols, const void 
  * transposed weights, whose square blocks keep their scales:
  * moe_fp8_transpose writes wt[n_matrices][K][N] and wt_scales
  * [n_matrices][ceil(K/128)][ceil(N/128)] from w [n_matrices][N][K] (N and K
- * positive multiples of 16), an exact copy to keep while w does not change.
+ * positive multiples of 16), an exact copy to keep while w does not change;
+ * n_matrices == 0 enqueues nothing.
  */
 int moe_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_t a_rows, const uint8_t *a,
                    const float *a_scales, const int32_t *row_map, const int32_t *expert_off, const uint8_t *w,

@@ -105,6 +105,9 @@ struct Fp8Args {
   float *hs;                 // gated tile kernel: h scales [ceil(N/128)][rows]
 };
 
+// Tiles of bm rows that n rows (any count of an int) take.
+__device__ __forceinline__ int tiles_in(int n, int bm) { return int((unsigned(n) + unsigned(bm) - 1) / unsigned(bm)); }
+
 // This workgroup's row tile and column block (false: none is left).  Each
 // XCD takes one contiguous range of the work, ordered in groups of 8 column
 // blocks with the tiles of an expert together, so that what neighbours share
@@ -129,12 +132,12 @@ __device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanI
     for (int e = e0; e < e1; ++e) {
       int lo, hi;
       range(e, lo, hi);
-      n += (hi - lo + bm - 1) / bm;
+      n += tiles_in(hi - lo, bm);
     }
     incl = wave_incl_scan(n);
     n_tiles = read_lane_i(incl, kWave - 1);
   } else {
-    n_tiles = (a.rows + bm - 1) / bm;
+    n_tiles = tiles_in(a.rows, bm);
   }
   const int work = n_tiles * nbx;  // the grid has at least as many workgroups
   if (lin >= work) return false;
@@ -148,7 +151,7 @@ __device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanI
       for (int e = e0; e < e1; ++e) {
         int lo, hi;
         range(e, lo, hi);
-        const int k = (hi - lo + bm - 1) / bm;
+        const int k = tiles_in(hi - lo, bm);
         if (tile < at + k) {
           fe = e;
           frow = lo + (tile - at) * bm;
@@ -889,7 +892,7 @@ void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, in
   g.out = y, g.out_dtype = out_dtype;
   const bool exact = out_dtype == MOE_DT_F32;
   const int bm = fp8_tile_rows(rows, N, K, n_experts, exact);
-  const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (rows + bm - 1) / bm;
+  const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (int64_t(rows) + bm - 1) / bm;
   if (bm == 16) launch_decode<kPlain>(g, tiles, s);
   else if (exact) launch_tile<kPlain, true>(g, bm, tiles, s);
   else if (bm <= 64) launch_tile<kPlain, false>(g, bm, tiles, s);

@@ -335,12 +335,12 @@ int moe_fp8_quantize(int32_t n_matrices, int32_t rows, int32_t cols, const void 
   int s;
   if (n_matrices < 0 || rows < 0 || cols <= 0 || cols % 16) return MOE_E_INVALID;
   if (!valid_dtype(dtype) || (block_rows != 1 && block_rows != 128)) return MOE_E_INVALID;
-  const int64_t all = int64_t(n_matrices) * rows, nbc = (cols + 127) / 128;
+  const int64_t all = int64_t(n_matrices) * rows, nbr = (int64_t(rows) + 127) / 128, nbc = (int64_t(cols) + 127) / 128;
   const bool none = all == 0;  // empty arrays may have no address
   if ((s = validate_ptr(x, none)) || (s = validate_ptr(codes, none)) || (s = validate_ptr(scales, none))) return s;
   if (none) return MOE_OK;
-  const int64_t groups = block_rows == 1 ? (all + 31) / 32 * nbc : int64_t(n_matrices) * ((rows + 127) / 128) * nbc;
-  if (all > INT32_MAX || groups > kMaxGroups) return MOE_E_INVALID;
+  if (all > INT32_MAX || nbc > kMaxGroups) return MOE_E_INVALID;
+  if ((block_rows == 1 ? (all + 31) / 32 : n_matrices * nbr) * nbc > kMaxGroups) return MOE_E_INVALID;
   if (block_rows == 1) launch_fp8_rows(x, dtype, int32_t(all), cols, codes, scales, stream);
   else launch_fp8_blocks(x, dtype, n_matrices, rows, cols, codes, scales, stream);
   return hip_status();
@@ -360,7 +360,8 @@ int moe_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, int32_
     return s;
   if (rows == 0) return MOE_OK;
   if (a_rows < (row_map ? 1 : rows)) return MOE_E_INVALID;
-  if (fp8_matmul_groups(rows, N, K, n_experts, expert_off != nullptr, out_dtype == MOE_DT_F32) > kMaxGroups) return MOE_E_INVALID;
+  if (fp8_matmul_groups(rows, N, K, n_experts, expert_off != nullptr, out_dtype == MOE_DT_F32) > kMaxGroups)
+    return MOE_E_INVALID;
   launch_fp8_matmul(rows, N, K, n_experts, a_rows, a, a_scales, row_map, expert_off, w, w_scales, y, out_dtype,
                     stream);
   return hip_status();
@@ -370,9 +371,12 @@ int moe_fp8_transpose(int32_t n_matrices, int32_t N, int32_t K, const uint8_t *w
                       float *wt_scales, void *stream) {
   int s;
   if (n_matrices < 0 || N <= 0 || K <= 0 || N % 16 || K % 16) return MOE_E_INVALID;
-  if ((s = validate_ptr(w)) || (s = validate_ptr(w_scales)) || (s = validate_ptr(wt)) || (s = validate_ptr(wt_scales)))
+  const bool none = n_matrices == 0;  // empty arrays may have no address
+  if ((s = validate_ptr(w, none)) || (s = validate_ptr(w_scales, none)) || (s = validate_ptr(wt, none)) ||
+      (s = validate_ptr(wt_scales, none)))
     return s;
-  if (int64_t(n_matrices) * ((N + 127) / 128) * ((K + 127) / 128) > kMaxGroups) return MOE_E_INVALID;
+  const int64_t blocks = (int64_t(N) + 127) / 128 * ((int64_t(K) + 127) / 128);
+  if (blocks > kMaxGroups || n_matrices * blocks > kMaxGroups) return MOE_E_INVALID;
   if (n_matrices == 0) return MOE_OK;
   launch_fp8_transpose(n_matrices, N, K, w, w_scales, wt, wt_scales, stream);
   return hip_status();

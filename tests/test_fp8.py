@@ -21,6 +21,8 @@ def lib():
     (1, 4, 16, A, 1, 1, None, A), (1, 4, 16, A, 1, 1, A, None), (1, 4, 16, A, 1, 1, A + 4, A),
     (1 << 20, 1 << 20, 16, A, 1, 1, A, A),       # more rows than an int32 counts
     (1 << 15, 1 << 10, 16 << 10, A, 1, 128, A, A),  # more workgroups than a grid holds
+    (1, (1 << 31) - 1, 16, A, 1, 128, A, A), (1, 1, (1 << 31) - 16, A, 1, 128, A, A),  # sizes that a rounding up overflows
+    (1, 1, (1 << 31) - 16, A, 1, 1, A, A), (1 << 30, 1 << 30, (1 << 31) - 16, A, 1, 1, A, A),
 ])
 def test_quantize_refusals(lib, args):
     assert lib.moe_fp8_quantize(*args, None) == moe.MOE_E_INVALID
@@ -55,9 +57,15 @@ def test_product_of_nothing(lib):
 @pytest.mark.parametrize("args", [
     (-1, 16, 16, A, A, A, A), (1, 8, 16, A, A, A, A), (1, 16, 0, A, A, A, A), (1, 16, 16, None, A, A, A),
     (1, 16, 16, A, A, A + 4, A), (1 << 24, 16, 16, A, A, A, A),
+    (1, (1 << 31) - 16, 16, A, A, A, A), (1, 16, (1 << 31) - 16, A, A, A, A),
+    ((1 << 31) - 1, (1 << 31) - 16, (1 << 31) - 16, A, A, A, A),
 ])
 def test_transpose_refusals(lib, args):
     assert lib.moe_fp8_transpose(*args, None) == moe.MOE_E_INVALID
+
+
+def test_transpose_of_nothing(lib):
+    assert lib.moe_fp8_transpose(0, 16, 16, None, None, None, None, None) == moe.MOE_OK
 
 
 def test_layer_refusals(lib):
