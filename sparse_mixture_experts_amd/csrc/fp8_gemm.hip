@@ -362,10 +362,13 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
     for (int mt = 0; mt < RB; ++mt) {
       const int m = mt * 16 + lr;
       if (m < tile.rows) {
+        // (codes of zero are not enough where a weight is a NaN)
+        const bool ok = source_row(a, tile.row0 + m) >= 0;
         const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
-          if (col0 + nt * 16 < a.N) store4(a, at + col0 + nt * 16, acc[nt][mt]);
+          if (col0 + nt * 16 < a.N)
+            store4(a, at + col0 + nt * 16, ok ? acc[nt][mt] : fp8_acc{0.f, 0.f, 0.f, 0.f});
       }
     }
   } else {
@@ -777,7 +780,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
   for (int nt = 0; nt < NTH; ++nt) {
     const int col = col0 + nt * 16;
     if (col < a.N) {
-      fp8_acc v = acc[nt];
+      fp8_acc v = rok ? acc[nt] : fp8_acc{0.f, 0.f, 0.f, 0.f};
       if constexpr (MODE == kGated) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = glu(acc[nt][i], acc[nt + NTH][i], a.round, a.geglu);

@@ -240,6 +240,20 @@ def test_product_bad_tables(rows, N, out):
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,N", [(20, 64), (130, 64), (700, 64), (5000, 1040), (9000, 2064), (17000, 4112)])
+def test_product_rows_outside_stay_zero_beside_nans(rows, N, out):
+    """A row of zeros stays one where the weights or their scales hold NaNs and infinities."""
+    K, E = 272, 4
+    case = list(product_case(rows, N, K, E, "random", True, rows))
+    case[5][::5] = -1
+    case[2][:, 3, 7] = 0x7F
+    case[3][:, -1, 1] = INF
+    y = run_product(case, rows, N, K, E, out)
+    assert (y[::5] == 0).all()
+    assert torch.isnan(y[1::5][:, 3]).all()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,N,E", [(6, 48, 1), (150, 48, 2), (5000, 1040, 2), (9000, 2064, 2), (17000, 4112, 1)])
 def test_product_padding_is_not_read(rows, N, E, out):
     """NaN codes outside a row's reduction (the next row's, a neighbour expert's) do not reach it."""
