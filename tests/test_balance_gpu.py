@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 U = 2.0**-24
 TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 # T, D, E, k, act, sequence lengths (None: no offsets), masked, bias, renorm
 CASES = [
@@ -426,3 +426,47 @@ def test_two_streams():
         for t, name in zip(o, ("logits", "counts", "tokens", "mean", "loss")):
             assert torch.equal(t.cpu(), want[name])
     assert math.isfinite(float(want["loss"]))
+
+
+@pytest.mark.parametrize("scale_x,scale_w", [(2.0**-18, 1.0), (1.0, 2.0**-17), (2.0**-20, 2.0**-3)])
+def test_subnormal_fp16_operands(scale_x, scale_w):
+    """fp16 values below 2^-14 count like others, in the logits and in every gradient."""
+    s = make(150, 136, 20, 3, "f16", [90, 60], True, False, True)
+    s["x"], s["w"] = (s["x"].float() * scale_x).half(), (s["w"].float() * scale_w).half()
+    assert ((s["x"].abs() < 2.0**-14) & (s["x"] != 0)).any() or ((s["w"].abs() < 2.0**-14) & (s["w"] != 0)).any()
+    o = forward(s)
+    l, rl = logits_64(s)
+    assert torch.all((o["logits"].double() - l).abs() <= rl)
+    check(backward(s, o), gradients_64(s, o, sequences(s)))
+
+
+@pytest.mark.parametrize("T", [20, 200])
+@pytest.mark.parametrize("low", [-INF, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_experts_closed_by_their_bias(T, low, renorm):
+    """A bias of -inf or of the lowest fp32 value takes an expert out: its probability and gradients are
+    zeros, and the others are what they are without it."""
+    E, closed = 70, [1, 20, 69]
+    open_ = [e for e in range(E) if e not in closed]
+    s = make(T, 64, E, 4, "bf16", [T // 2, T - T // 2], False, True, renorm)
+    keep = torch.tensor(open_)
+    s["idx"] = keep[torch.rand((T, len(open_)), generator=torch.Generator().manual_seed(1)).argsort(dim=1)[:, :4]]
+    s["idx"] = s["idx"].to(torch.int32).contiguous()
+    s["bias"][closed] = low
+    o = forward(s)
+    r = backward(s, o)
+    assert (o["mean"][:, closed] == 0).all() and (o["counts"][:, closed] == 0).all()
+    assert (r["db"][closed] == 0).all() and (r["dw"][:, closed] == 0).all()
+    # in 64 bits over the open experts: every probability within the fp32 softmax's radius
+    here = sequences(s)
+    l, rl = logits_64(s)
+    l, rl = l[:, open_], rl[:, open_]
+    p, rp = torch.softmax(l, dim=1), softmax_radius(l, rl)
+    n = here.sum(dim=1).double()[:, None]
+    mean = here.double() @ p / n
+    assert torch.all((o["mean"][:, open_].double() - mean).abs() <= here.double() @ (p * rp) / n + (T + 16) * 2 * U * mean)
+    counts = torch.stack([torch.bincount(s["idx"][h].long().flatten(), minlength=E) for h in here]).double()
+    loss = (E / (4 * n[:, 0]) * (counts[:, open_] * mean).sum(dim=1)).mean()
+    rel = float(rp.max()) + (T + E + 60) * 2 * U
+    assert abs(float(o["loss"]) - float(loss)) <= rel * float(loss)
+    assert all(torch.isfinite(v).all() for v in r.values())
