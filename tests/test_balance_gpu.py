@@ -470,3 +470,44 @@ def test_experts_closed_by_their_bias(T, low, renorm):
     rel = float(rp.max()) + (T + E + 60) * 2 * U
     assert abs(float(o["loss"]) - float(loss)) <= rel * float(loss)
     assert all(torch.isfinite(v).all() for v in r.values())
+
+
+def test_longest_batch():
+    """2^20 tokens and 1024 experts (2^30 logits, 3 * 2^30 pieces of their gradients): every 1024 tokens
+    repeat the first ones, so do their logits and gradients, and the counts are multiples."""
+    P, T, D, E, k = 1024, 1 << 20, 64, 1024, 2
+    s = make(P, D, E, k, "bf16", None, False, True, True)
+    small = forward(s)
+    here = sequences(s)
+    n = T // P
+    big = dict(s, T=T)
+    for name in ("x", "idx", "dtopk"):
+        big[name] = s[name].repeat(n, 1)
+    a = {name: dev(big[name]) for name in ("x", "w", "bias", "idx", "dtopk")}
+    logits = torch.empty((T, E), device=DEV)
+    counts, tokens = torch.empty((1, E), dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    mean, loss = torch.empty((1, E), device=DEV), torch.empty(1, device=DEV)
+    ws = torch.empty(moe.moe_balance_workspace_size(s["desc"], T, 1), dtype=torch.uint8, device=DEV)
+    moe.moe_balance_loss(s["desc"], T, a["x"], a["w"], a["bias"], a["idx"], None, 1, None, logits, counts, tokens, mean,
+                         loss, ws)
+    assert (logits.view(n, P, E) == logits[:P]).all()
+    l, rl = logits_64(s)
+    assert torch.all((logits[:P].cpu().double() - l).abs() <= rl)
+    assert int(tokens) == T and torch.equal(counts.cpu(), n * small["counts"])
+    # the logits' reduction is split otherwise; sums of T probabilities: a chunk's, then the records'
+    rel = 2 * float(softmax_radius(l, rl).max()) + (128 + T // 128 + 16 + P + 2 * E) * 2 * U
+    assert abs(float(loss) - float(small["loss"])) <= rel * float(small["loss"])
+    dx, dw, db = torch.empty((T, D), device=DEV), torch.empty((D, E), device=DEV), torch.empty(E, device=DEV)
+    moe.moe_balance_loss_backward(s["desc"], T, a["x"], a["w"], a["idx"], None, 1, None, logits, counts, tokens,
+                                  None, a["dtopk"], dx, dw, db, ws)
+    assert (dx.view(n, P, D) == dx[:P]).all()
+    # the first period against the formula: its loss part is that of n times as many tokens
+    part = dict(s, dloss=torch.tensor([1.0 / n]))
+    o = dict(small, logits=logits[:P].cpu())
+    want = gradients_64(part, o, here)
+    check({"dx": dx[:P].cpu()}, want)
+    # n such periods; their sums take up to T additions, each of half a step of sum |x||dl|, of which the
+    # radius of one period holds P + 48 (dW) and P + 16 (dbias)
+    (cw, rw), (cb, rb) = want["dw"], want["db"]
+    assert torch.all((dw.cpu().double() - n * cw).abs() <= n * rw * (1 + (T + 48) / (P + 48)))
+    assert torch.all((db.cpu().double() - n * cb).abs() <= n * rb * (1 + (T + 16) / (P + 16)))

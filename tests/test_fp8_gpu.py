@@ -503,3 +503,59 @@ def test_work_of_many_experts_and_rows():
     y = run_product(case, rows, N, K, E, "f32")
     check_product(case, y, rows, N, K, E, "f32")
     assert np.isfinite(y.numpy()).all()
+
+
+def test_weights_past_32_bits():
+    """The last of 520 matrices, 4 GiB into the codes: quantised, transposed and multiplied to the same
+    bits as the first one, which holds the same values (every kernel of the grouped product)."""
+    E, N, K = 520, 4096, 2048
+    x = torch.randn((E, N, K), device=DEV, dtype=torch.bfloat16)
+    x[0] = x[E - 1]
+    w = torch.empty((E, N, K), dtype=torch.uint8, device=DEV)
+    sw = torch.empty((E, ref.nb(N), ref.nb(K)), device=DEV)
+    moe.moe_fp8_quantize(E, N, K, x, DT["bf16"], 128, w, sw)
+    c, s = quantize(x[E - 1:].cpu(), "bf16", 128)
+    assert torch.equal(w[E - 1].cpu(), c[0]) and torch.equal(sw[E - 1].cpu(), s[0])
+    del x
+    wt, st = torch.empty((E, K, N), dtype=torch.uint8, device=DEV), torch.empty((E, ref.nb(K), ref.nb(N)), device=DEV)
+    moe.moe_fp8_transpose(E, N, K, w, sw, wt, st)
+    assert torch.equal(wt[E - 1], w[E - 1].t()) and torch.equal(st[E - 1], sw[E - 1].t())
+    del wt
+    a_rows = 97
+    a, sa = quantize(torch.randn((1, a_rows, K), generator=gen(2)).bfloat16(), "bf16", 1)
+    rv, wv = ref.row_values(a[0], sa)[:16], ref.matrix_values(w[E - 1:].cpu(), sw[E - 1:].cpu())[0]
+    a, sa = a[0].to(DEV), sa.to(DEV)
+    for rows, out in ((100, "f32"), (9000, "f32"), (18000, "bf16"), (24000, "bf16"), (52000, "bf16")):
+        print(f"[case] {rows} rows {out}", flush=True)
+        row_map = (torch.arange(rows) % a_rows).to(torch.int32).to(DEV)
+        y = [torch.empty((rows, N), dtype=ref.TORCH[out], device=DEV) for _ in range(2)]
+        for i, e in enumerate((0, E - 1)):
+            off = torch.full((E + 1,), rows, dtype=torch.int32)
+            off[:e + 1] = 0
+            moe.moe_fp8_matmul(rows, N, K, E, a_rows, a, sa, row_map, off.to(DEV), w, sw, y[i], DT[out])
+        assert torch.equal(y[0], y[1])
+        c, r = ref.product(rv, wv)
+        if out != "f32":
+            r = r + ref.dropped(rv, wv)
+        bound = r + torch.finfo(ref.TORCH[out]).eps / 2 * (c.abs() + r) + 1e-38
+        assert torch.all((y[1][:16].cpu().double() - c).abs() <= bound)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_results_past_32_bits(out):
+    """530000 x 4112 results: the last rows, past 2^31 of them, repeat the first ones' bits."""
+    rows, N, K, a_rows = 530000, 4112, 144, 1000
+    a, sa, w, sw = (t.to(DEV) for t in product_case(a_rows - 2, N, K, 1, None, False, 3)[:4])
+    row_map = (torch.arange(rows) % a_rows).to(torch.int32).to(DEV)
+    y = torch.empty((rows, N), dtype=ref.TORCH[out], device=DEV)
+    moe.moe_fp8_matmul(rows, N, K, 1, a_rows, a, sa, row_map, None, w, sw, y, DT[out])
+    assert torch.equal(y[529000:], y[:1000])
+    x = y[528900:].float()  # and rows whose elements lie past 2^31, quantised
+    del y
+    big = torch.zeros((rows, N), dtype=torch.bfloat16, device=DEV)
+    big[528900:] = x.bfloat16()
+    codes = torch.empty((rows, N), dtype=torch.uint8, device=DEV)
+    scales = torch.empty((ref.nb(N), rows), device=DEV)
+    moe.moe_fp8_quantize(1, rows, N, big, DT["bf16"], 1, codes, scales)
+    c, s = quantize(big[528900:][None].cpu(), "bf16", 1)
+    assert torch.equal(codes[528900:].cpu(), c[0]) and torch.equal(scales[:, 528900:].cpu(), s)
