@@ -14,9 +14,9 @@
 //   dl the softmax backward of the slot weights from dw            (kernel 5)
 // The forward's per-op rounding is not differentiated (the unrounded GLU).
 // fp32 and fp8 layers run kernels 1-4 here (fp8 weights as scale * code, x as
-// it is: the rounding to codes is not differentiated either), all arithmetic fp32 on the vector units
-// (each weight element is read where its row or column is reduced, for up to
-// kMR routed rows at a time); 16-bit layers run the matrix-core versions of
+// it is: the rounding to codes is not differentiated either), all arithmetic
+// fp32 on the vector units (each weight element is read where its row or
+// column is reduced, for up to kMR routed rows at a time); 16-bit layers run the matrix-core versions of
 // kernels 1-4 (backward_mfma.hip).  Kernel 5 serves both.
 #include <hip/hip_runtime.h>
 

@@ -7,18 +7,20 @@
 // The sum over one block is one v_mfma_f32_16x16x128_f8f6f4 or four
 // v_mfma_f32_16x16x32_f16 (fp8_common.h), started from zero, whose four
 // results per lane one fma each brings to the running fp32 sum with the
-// block's scale: 16 vector cycles beside 32 or 64 matrix cycles.  Operand a holds 16 weight rows n and operand b 16 token rows, so a lane's
-// results are 4 consecutive outputs of one token and its scale is one value.
-// Lane group g = lane / 16 holds bytes 16 g .. +15 and 64 + 16 g .. +15 of the
-// 128 (of both operands), so each 16-byte load of a wave covers whole 64-byte
-// pieces of 16 rows.
+// block's scale: 16 vector cycles beside 32 or 64 matrix cycles.  Operand a
+// holds 16 weight rows n and operand b 16 token rows, so a lane's results are
+// 4 consecutive outputs of one token and its scale is one value.  Lane group
+// g = lane / 16 holds bytes 16 g .. +15 and 64 + 16 g .. +15 of the 128 (of
+// both operands).
 //
-// Three kernels.  The tile kernel (experts with many rows) takes 64 token
-// rows by 256 weight rows, the wide one 128 by 256: the rows' codes go through
-// LDS, double buffered, the weights straight from memory to the registers of
-// the one wave that uses them.  The decode kernel (few rows per expert) is
-// bound by the weights' bytes: the waves of a workgroup split the reduction,
-// each with several blocks of weights in flight, and add up through LDS.
+// Four kernels, by rows per expert: the decode kernel (16 rows a tile), the
+// tile kernel (32, 48 or 64), and for the 8-bit instruction the wide and the
+// huge one (128 and 256).  Where an expert has few rows the weights' bytes
+// are the bound, so they are loaded as they lie in memory, whole 128-byte
+// rows, several blocks ahead of their use, and turned into the operand's
+// layout through LDS.  (Loaded in the operand's layout directly, neighbouring
+// lanes are in different rows and every load met 64 cache lines: about 28 ns
+// of a CU's address path each, which bounded all four kernels.)
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -198,10 +200,13 @@ __device__ __forceinline__ void store4(const Fp8Args &a, int64_t at, const fp8_a
   }
 }
 
-// The tile of 16 RB token rows (32, 48 or 64).  Weights and rows are requested
-// two blocks ahead of their use, into two sets of registers: with one block
-// in flight a workgroup waited out a memory round trip per block.  EXACT: see
-// Fp8Operand.
+// The tile of 16 RB token rows (32, 48 or 64) by 256 weight rows.  Weights
+// and rows are requested two blocks ahead of their use, into two sets of
+// registers: with one block in flight a workgroup waited out a memory round
+// trip per block.  EXACT: see Fp8Operand.  Bound by the weights' bytes: gate
+// and up of 512 experts of 2048 x 512 at 40 rows each (1.07 GB) take 238 us
+// with the exact sums, 4.5 TB/s, and down (0.54 GB and 168 MB of results)
+// 151 us, 4.7 TB/s, where a large copy reaches 5.1.
 template <int RB, int MODE, bool EXACT>
 __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
   constexpr int BM = RB == 2 ? 32 : 64;             // rows that are staged (zeros past the tile's)
@@ -417,7 +422,11 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
 // cores bound.  128 token rows by 64 weight rows per wave are 32 products of
 // 32 cycles for 16 KB read from LDS and 8 KB from memory, so that with two
 // waves per SIMD neither path (128 and 64 bytes a cycle) is near its limit.
-// The rows go from memory to LDS without passing through registers.
+// The rows go from memory to LDS without passing through registers.  4096
+// rows, N = 4096, K = 2048: 51 us, 1.35 PFLOP/s (the tile kernel 66).  Neither
+// memory, LDS nor the fmas alone bound it: left out one by one in timing
+// copies, each changed it by a few percent.  What is left are the waits of
+// two workgroups per CU at one barrier per block.
 __global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
   constexpr int RB = 8, BM = RB * 16, PASS = BM * kPieces / kThreads;  // 4
   __shared__ __align__(16) uint8_t sa0[BM * kFp8Block], sa1[BM * kFp8Block];
@@ -548,7 +557,9 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
 // The 256-row tile, for large products: 8 waves of 128 token rows by 64
 // weight rows, both operands from memory to LDS without passing through
 // registers and read from there as they are used (24 KB for a wave's 32
-// products).  One workgroup fills a CU.
+// products).  One workgroup fills a CU.  8192 x 5632 x 2048: 122 us, 1.55
+// PFLOP/s; the instruction alone, fed from registers with random codes,
+// reaches 3.7, and a bf16 product of the library 1.2.
 constexpr int kHugeRows = 256;
 constexpr int kHugeThreads = 512;
 __global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
@@ -671,7 +682,12 @@ __global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
 }
 
 // The decode kernel: 16 token rows by WN weight tiles per wave; KW of the
-// four waves split the reduction, the others take further columns.
+// four waves split the reduction, the others take further columns.  Bound by
+// the weights' bytes: 32 tokens' down (111 experts' 2048 x 768, 181 MB with
+// the results) 39.6 us, 4.6 TB/s; one token's 8 experts of 1536 x 2048 (25 MB)
+// 8.2 us, of which a launch and one memory round trip are about 4.  Each wave
+// keeps DEPTH blocks in flight in registers (a ring in LDS filled by direct
+// loads was drained by the compiler at every step, and lost).
 template <int KW, int WN, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
   constexpr int NTH = MODE == kGated ? WN / 2 : WN;
@@ -792,8 +808,6 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
 
 // Row tiles that the experts' rows can take at most: each expert adds at most
 // one partly filled tile.
-
-
 int64_t most_tiles(int64_t rows, int experts, int bm) {
   return rows / bm + std::min<int64_t>(rows, experts);
 }
@@ -853,9 +867,6 @@ void launch_decode(const Fp8Args &a, int64_t tiles, hipStream_t s) {
 // the GPU at most about once over, or at most 16 rows an expert; 64 while its
 // workgroups fit the GPU at once, or experts would leave a larger tile half
 // empty; 256 from two of its tiles per CU on.
-int fp8_small_tile(int64_t rows, int experts) {
-  return rows <= 26LL * experts ? 32 : rows <= 42LL * experts ? 48 : 64;
-}
 int fp8_tile_rows(int64_t rows, int32_t N, int32_t K, int experts, bool exact) {
   const int64_t t16 = most_tiles(rows, experts, 16), t64 = rows / 64 + experts / 2;
   const int dc = decode_cols(K, false), nbx = (N + kBN - 1) / kBN;
@@ -863,6 +874,15 @@ int fp8_tile_rows(int64_t rows, int32_t N, int32_t K, int experts, bool exact) {
   if (rows <= 42LL * experts) return fp8_small_tile(rows, experts);
   if (exact || rows < 96LL * experts || t64 * nbx <= 640) return 64;
   return rows / kHugeRows * nbx >= 512 && rows >= 1024LL * experts ? 256 : 128;
+}
+
+// For experts with few rows, the smallest tile that holds the mean with room:
+// rows of a tile that no token fills cost products all the same.  Gate/up and
+// down of the 512-expert layer at 40 rows an expert 247 and 155 us with 64
+// rows, 238 and 151 with 48, 298 and 181 with 32 (experts above the mean then
+// read their weights twice).
+int fp8_small_tile(int64_t rows, int experts) {
+  return rows <= 26LL * experts ? 32 : rows <= 42LL * experts ? 48 : 64;
 }
 
 int64_t fp8_matmul_groups(int64_t rows, int32_t N, int32_t K, int32_t n_experts, bool offsets, bool exact) {
