@@ -15,13 +15,15 @@
 //
 // Four kernels, by rows per expert: the decode kernel (16 rows a tile), the
 // tile kernel (32, 48 or 64), and for the 8-bit instruction the wide and the
-// huge one (128 and 256).  Where an expert has few rows the weights' bytes
+// huge one (128 and 256); a fifth holds the tile and the wide one, for experts
+// of unequal numbers of rows.  Where an expert has few rows the weights' bytes
 // are the bound, so they are loaded as they lie in memory, whole 128-byte
 // rows, several blocks ahead of their use, and turned into the operand's
 // layout through LDS.  (Loaded in the operand's layout directly, neighbouring
 // lanes are in different rows and every load met 64 cache lines: about 28 ns
 // of a CU's address path each, which bounded all four kernels.)
 #include <algorithm>
+#include <climits>
 
 #include "fp8_common.h"
 #include "launch.h"
@@ -35,6 +37,9 @@ constexpr int kNW = kThreads / kWave;
 constexpr int kNT = 4;                    // 16-row weight tiles per wave of the tile kernel
 constexpr int kBN = kNW * kNT * 16;       // weight rows per workgroup (256)
 constexpr int kPieces = kFp8Block / 16;   // 16-byte pieces per row and block (8)
+constexpr int kWideRows = 128;            // rows of the wide tile
+constexpr int kWideFrom = 96;             // rows of an expert from which the mixed kernel takes them
+constexpr int kBigTile = 1 << 30;         // my_work: a wide tile among small ones
 
 __device__ __forceinline__ uint4 keep(const uint4 &v, bool ok) {
   return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
@@ -119,9 +124,16 @@ __device__ __forceinline__ int tiles_in(int n, int bm) { return int((unsigned(n)
 // in tiles of bm are counted 64 at a time, one prefix sum gives the number of
 // tiles, and the lane whose range holds this one's number looks it up.
 // Ranges are read as if clamped to [0, rows].
-__device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanItem &t, int &bx) {
-  const int lin = int(blockIdx.x), lane = lane_id();
+//
+// `wide`: experts with at least that many rows are in tiles of kWideRows
+// (their rows come with kBigTile), which all go before the others' tiles: a
+// long workgroup that starts last would be waited for.
+template <bool MIXED = false>
+__device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanItem &t, int &bx, int wide = 0) {
+  int lin = int(blockIdx.x);
+  const int lane = lane_id();
   int n_tiles, incl = 0, n = 0, e0 = 0, e1 = 0;
+  bool big = false;  // MIXED: this workgroup's tile is a wide one
   auto range = [&](int e, int &lo, int &hi) {
     lo = min(max(a.expert_off[e], 0), a.rows);
     hi = min(max(a.expert_off[e + 1], lo), a.rows);
@@ -131,12 +143,22 @@ __device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanI
   } else if (a.expert_off) {
     const int per = (a.E + kWave - 1) / kWave;
     e0 = lane * per, e1 = min(e0 + per, a.E);
+    int nw = 0;
     for (int e = e0; e < e1; ++e) {
       int lo, hi;
       range(e, lo, hi);
-      n += tiles_in(hi - lo, bm);
+      if (MIXED && hi - lo >= wide) nw += tiles_in(hi - lo, kWideRows);
+      else n += tiles_in(hi - lo, bm);
     }
-    incl = wave_incl_scan(n);
+    if constexpr (MIXED) {
+      const int inclw = wave_incl_scan(nw), first = read_lane_i(inclw, kWave - 1) * nbx;
+      big = lin < first;
+      if (!big) lin -= first;
+      incl = wave_incl_scan(big ? nw : n);
+      n = big ? nw : n;
+    } else {
+      incl = wave_incl_scan(n);
+    }
     n_tiles = read_lane_i(incl, kWave - 1);
   } else {
     n_tiles = tiles_in(a.rows, bm);
@@ -148,16 +170,17 @@ __device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanI
   if (a.tiles) {
     t = a.tiles[tile];
   } else if (a.expert_off) {
+    const int m = big ? kWideRows : bm;
     int at = incl - n, fe = 0, frow = 0, frows = 0;
     if (tile >= at && tile < incl) {
       for (int e = e0; e < e1; ++e) {
         int lo, hi;
         range(e, lo, hi);
-        const int k = tiles_in(hi - lo, bm);
+        const int k = MIXED && (hi - lo >= wide) != big ? 0 : tiles_in(hi - lo, m);
         if (tile < at + k) {
           fe = e;
-          frow = lo + (tile - at) * bm;
-          frows = min(bm, hi - frow);
+          frow = lo + (tile - at) * m;
+          frows = min(m, hi - frow);
           break;
         }
         at += k;
@@ -175,6 +198,7 @@ __device__ __forceinline__ bool my_work(const Fp8Args &a, int bm, int nbx, PlanI
   t.expert = __builtin_amdgcn_readfirstlane(t.expert);
   t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
   t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  if (MIXED && big) t.rows |= kBigTile;
   return true;
 }
 
@@ -207,31 +231,32 @@ __device__ __forceinline__ void store4(const Fp8Args &a, int64_t at, const fp8_a
 // and up of 512 experts of 2048 x 512 at 40 rows each (1.07 GB) take 238 us
 // with the exact sums, 4.5 TB/s, and down (0.54 GB and 168 MB of results)
 // 151 us, 4.7 TB/s, where a large copy reaches 5.1.
-template <int RB, int MODE, bool EXACT>
-__global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
-  constexpr int BM = RB == 2 ? 32 : 64;             // rows that are staged (zeros past the tile's)
-  constexpr int NP = 2;                             // weight tiles that a read of the rows serves
+template <int RB, bool EXACT>
+struct TileLds {
+  static constexpr int BM = RB == 2 ? 32 : 64;  // rows that are staged (zeros past the tile's)
   // rows in LDS: codes, or (EXACT) fp16, turned into it once here instead of
   // by every wave for every weight tile; 16 bytes of padding put the pieces
   // that 16 lanes read together, one of 16 rows each, on different banks
-  constexpr int XB = EXACT ? 2 : 1, ROW = kFp8Block * XB + 16;
+  static constexpr int XB = EXACT ? 2 : 1, ROW = kFp8Block * XB + 16;
+  static constexpr int NSL = kThreads / BM;     // one scale per thread
+  using Rows = uint8_t[2][BM][ROW];
+  using Scales = float[2][NSL][BM];             // row scale * weight scale
+  using Max = float[kNW][BM];
+};
+using Turn = uint8_t[kNW][kNT][kTileBytes];
+template <int RB, int MODE, bool EXACT>
+__device__ __forceinline__ void tile_body(const Fp8Args &a, const PlanItem &tile, int bx, typename TileLds<RB, EXACT>::Rows &sa,
+                                          Turn &turn, typename TileLds<RB, EXACT>::Scales &ss,
+                                          typename TileLds<RB, EXACT>::Max &rmax) {
+  constexpr int BM = TileLds<RB, EXACT>::BM, XB = TileLds<RB, EXACT>::XB, NSL = TileLds<RB, EXACT>::NSL;
+  constexpr int NP = 2;                             // weight tiles that a read of the rows serves
   constexpr int PPT = BM * kPieces / kThreads;      // 16-byte pieces of the rows per thread
   constexpr int NTH = MODE == kGated ? kNT / 2 : kNT;
   constexpr int COLS = kNW * NTH * 16;              // output columns per workgroup
   // weight scale blocks that a workgroup meets: 256 rows cover two; gated:
   // one of gate rows, and two of up rows when they start inside a block
   constexpr int NS = MODE == kGated ? 3 : 2;
-  constexpr int NSL = kThreads / BM;                // one scale per thread (those past NS repeat the last)
   static_assert(NS <= NSL && RB * 16 <= BM, "one scale per thread");
-  __shared__ __align__(16) uint8_t sa[2][BM][ROW];
-  __shared__ __align__(16) uint8_t turn[kNW][kNT][kTileBytes];
-  __shared__ float ss[2][NSL][BM];                  // row scale * weight scale
-  __shared__ float rmax[MODE == kGated ? kNW : 1][BM];
-
-  const int nbx = (a.N + COLS - 1) / COLS;
-  PlanItem tile;
-  int bx;
-  if (!my_work(a, RB * 16, nbx, tile, bx)) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = lane_id();
   const int lr = lane & 15, lg = lane >> 4;
   const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
@@ -418,6 +443,20 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
   }
 }
 
+template <int RB, int MODE, bool EXACT>
+__global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
+  using L = TileLds<RB, EXACT>;
+  __shared__ __align__(16) typename L::Rows sa;
+  __shared__ __align__(16) Turn turn;
+  __shared__ typename L::Scales ss;
+  __shared__ typename std::conditional<MODE == kGated, typename L::Max, float>::type rmax;
+  constexpr int COLS = MODE == kGated ? kBN / 2 : kBN;
+  PlanItem tile;
+  int bx;
+  if (my_work(a, RB * 16, (a.N + COLS - 1) / COLS, tile, bx))
+    tile_body<RB, MODE, EXACT>(a, tile, bx, sa, turn, ss, reinterpret_cast<typename L::Max &>(rmax));
+}
+
 // The 128-row tile of the 8-bit instruction, for products that the matrix
 // cores bound.  128 token rows by 64 weight rows per wave are 32 products of
 // 32 cycles for 16 KB read from LDS and 8 KB from memory, so that with two
@@ -427,16 +466,12 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
 // memory, LDS nor the fmas alone bound it: left out one by one in timing
 // copies, each changed it by a few percent.  What is left are the waits of
 // two workgroups per CU at one barrier per block.
-__global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
+__device__ __forceinline__ void wide_body(const Fp8Args &a, const PlanItem &tile, int bx, uint8_t *sa0, uint8_t *sa1,
+                                          Turn &turn, float *ssp0, float *ssp1) {
   constexpr int RB = 8, BM = RB * 16, PASS = BM * kPieces / kThreads;  // 4
-  __shared__ __align__(16) uint8_t sa0[BM * kFp8Block], sa1[BM * kFp8Block];
-  __shared__ __align__(16) uint8_t turn[kNW][kNT][kTileBytes];
-  __shared__ float ss0[2][BM], ss1[2][BM];  // row scale * scale of either block of 128 weight rows
-
-  const int nbx = (a.N + kBN - 1) / kBN;
-  PlanItem tile;
-  int bx;
-  if (!my_work(a, BM, nbx, tile, bx)) return;
+  // row scale * scale of either block of 128 weight rows
+  auto &ss0 = *reinterpret_cast<float (*)[2][BM]>(ssp0);
+  auto &ss1 = *reinterpret_cast<float (*)[2][BM]>(ssp1);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = lane_id();
   const int lr = lane & 15, lg = lane >> 4;
   const int K = a.K, nb = (K + kFp8Block - 1) / kFp8Block;
@@ -551,6 +586,45 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
         if (col0 + nt * 16 < a.N)
           store4(a, at + col0 + nt * 16, ok ? acc[nt][mt] : fp8_acc{0.f, 0.f, 0.f, 0.f});
     }
+  }
+}
+
+__global__ __launch_bounds__(kThreads, 2) void fp8_wide_kernel(Fp8Args a) {
+  __shared__ __align__(16) uint8_t sa0[kWideRows * kFp8Block], sa1[kWideRows * kFp8Block];
+  __shared__ __align__(16) Turn turn;
+  __shared__ float ss0[kThreads], ss1[kThreads];
+  PlanItem tile;
+  int bx;
+  if (my_work(a, kWideRows, (a.N + kBN - 1) / kBN, tile, bx)) wide_body(a, tile, bx, sa0, sa1, turn, ss0, ss1);
+}
+
+// Both in one grid, since experts' numbers of rows differ: the wide tile for
+// experts with kWideFrom rows or more, the small one (the mean's size) for the
+// others.  An expert with many rows in small tiles reads its weights from L2
+// once per tile and pays each tile's waits.  Small tiles alone / mixed from
+// 96 / 129 / 257 rows on, us: 20480 skewed rows over 512 experts of
+// 1024 x 2048, about a third of them touched, 153 / 133 / 133 / 134; all
+// touched 268 / 260 / 262 / 265; evenly spread 227 / 230 / 229 / 230; 4096
+// rows over 128 experts of 2048 x 1024 59 / 56 / 57 / 58, over 32 experts of
+// 1024 x 2048 36 / 30 / 30 / 35.
+template <int RB>
+__global__ __launch_bounds__(kThreads, 2) void fp8_mixed_kernel(Fp8Args a) {
+  using L = TileLds<RB, false>;
+  constexpr int WIDE = kWideRows * kFp8Block;
+  __shared__ __align__(16) uint8_t sa0[std::max<int>(sizeof(typename L::Rows), WIDE)], sa1[WIDE];
+  __shared__ __align__(16) Turn turn;
+  __shared__ float ss0[2 * kThreads], ss1[kThreads];
+  static_assert(sizeof(typename L::Scales) == sizeof(ss0), "the small tile's scales");
+  PlanItem tile;
+  int bx;
+  if (!my_work<true>(a, RB * 16, (a.N + kBN - 1) / kBN, tile, bx, kWideFrom)) return;
+  if (tile.rows & kBigTile) {
+    tile.rows &= ~kBigTile;
+    wide_body(a, tile, bx, sa0, sa1, turn, ss0, ss1);
+  } else {
+    tile_body<RB, kPlain, false>(a, tile, bx, reinterpret_cast<typename L::Rows &>(sa0), turn,
+                                 reinterpret_cast<typename L::Scales &>(ss0),
+                                 reinterpret_cast<typename L::Max &>(ss1));  // (no maxima in a plain product)
   }
 }
 
@@ -822,6 +896,13 @@ void launch_tile(const Fp8Args &a, int bm, int64_t tiles, hipStream_t s) {
   else if (bm == 48) launch((fp8_tile_kernel<3, MODE, EXACT>), grid, dim3(kThreads), 0, s, a);
   else launch((fp8_tile_kernel<4, MODE, EXACT>), grid, dim3(kThreads), 0, s, a);
 }
+void launch_mixed(const Fp8Args &a, int bm, int64_t tiles, hipStream_t s) {
+  const int64_t nbx = (a.N + kBN - 1) / kBN;
+  const dim3 grid(unsigned(tiles * nbx));
+  if (bm == 32) launch(fp8_mixed_kernel<2>, grid, dim3(kThreads), 0, s, a);
+  else if (bm == 48) launch(fp8_mixed_kernel<3>, grid, dim3(kThreads), 0, s, a);
+  else launch(fp8_mixed_kernel<4>, grid, dim3(kThreads), 0, s, a);
+}
 void launch_wide(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   const int64_t nbx = (a.N + kBN - 1) / kBN;
   launch(fp8_wide_kernel, dim3(unsigned(tiles * nbx)), dim3(kThreads), 0, s, a);
@@ -918,6 +999,7 @@ void launch_fp8_matmul(int32_t rows, int32_t N, int32_t K, int32_t n_experts, in
   const int64_t tiles = expert_off ? most_tiles(rows, n_experts, bm) : (int64_t(rows) + bm - 1) / bm;
   if (bm == 16) launch_decode<kPlain>(g, tiles, s);
   else if (exact) launch_tile<kPlain, true>(g, bm, tiles, s);
+  else if (bm <= 64 && expert_off && n_experts > 1) launch_mixed(g, bm, tiles, s);
   else if (bm <= 64) launch_tile<kPlain, false>(g, bm, tiles, s);
   else if (bm == 128) launch_wide(g, tiles, s);
   else launch_huge(g, tiles, s);

@@ -222,6 +222,21 @@ def test_product(rows, N, K, E, kind, gathered, out):
     assert torch.equal(y.view(torch.uint8), run_product(case, rows, N, K, E, out).view(torch.uint8))
 
 
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("E,N,K", [(60, 2320, 272), (36, 3088, 144), (20, 3600, 400)])  # 32, 48 and 64 rows a small tile
+def test_product_unequal_experts(E, N, K, out):
+    """Experts on both sides of every tile's border side by side, some without rows."""
+    counts = [95, 0, 96, 1, 97, 300, 17, 128, 129, 64, 0, 255, 2, 33]
+    counts += [1] * (E - len(counts))
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+    rows = int(off[-1]) + 5  # the last five belong to no expert
+    case = list(product_case(rows, N, K, E, "random", True, E))
+    case[4] = off
+    y = run_product(case, rows, N, K, E, out)
+    check_product(case, y, rows, N, K, E, out)
+    assert torch.equal(y.view(torch.uint8), run_product(case, rows, N, K, E, out).view(torch.uint8))
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,N", [(20, 64), (700, 64), (5000, 1040), (9000, 2064), (17000, 4112)])
 def test_product_bad_tables(rows, N, out):
