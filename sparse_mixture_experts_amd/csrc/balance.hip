@@ -462,6 +462,100 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
   }
 }
 
+// dx = dl W^T for at most 64 KS experts: a workgroup keeps the pieces of its 64
+// tokens' dl in registers, as operands, and runs over column tiles of W, two
+// steps ahead (a reduction this short is over before a workgroup of its own
+// for every 64 x 64 results has its operands).
+template <int DT, bool VECB, int KS>
+__global__ __launch_bounds__(kThreads, 2) void balance_dx_kernel(GemmArgs g, int per_wg) {
+  using SB = Stage<DT, true, false, VECB>;
+  constexpr int PA = kPieces, PB = SB::P, S = 2;
+  __shared__ __align__(16) uint16_t lb[2][PB][kTile * kStep];
+  const int lane = lane_id(), wave = threadIdx.x / kWave, lr = lane & 15, lg = lane >> 4;
+  const int m0 = blockIdx.y * kTile, wm = (wave >> 1) * 16 * S, wn = (wave & 1) * 16 * S;
+  const int N = g.b.rows, nt0 = blockIdx.x * per_wg, nt1 = min(nt0 + per_wg, (N + kTile - 1) / kTile);
+  const int Kl = (g.K + 7) / 8 * 8;
+  auto start_of = [&](int s) { return max(0, min(s * kStep, Kl - kStep)); };
+  uint4 fa[KS][2][PA][S];  // (elements past K meet zeros of the other operand)
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int p = 0; p < PA; ++p)
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const int64_t row = min(m0 + wm + i * 16 + lr, g.a.rows - 1);
+          const int k = min(start_of(s) + h * 32 + lg * 8, int(g.a.ld) - 8);
+          fa[s][h][p][i] =
+              *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(g.a.p) + p * g.a.plane + row * g.a.ld + k);
+        }
+  f32x4 acc[S][S];
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  SB sb[2];
+  const int total = (nt1 - nt0) * KS;  // steps: the KS of one column tile after another
+  auto load = [&](int q, auto rc) {
+    sb[decltype(rc)::value].template load<false>(g.b, (nt0 + q / KS) * kTile, start_of(q % KS), g.K, g.tokens, 0, 0);
+  };
+  auto store = [&](int q, auto rc) {
+    constexpr int r = decltype(rc)::value;
+    sb[r].store(lb[r], start_of(q % KS), q % KS * kStep, g.K);
+  };
+  auto step = [&](int q, auto rc, auto next) {
+    constexpr int r = decltype(rc)::value, s = KS == 2 ? r : 0;
+    if (q + 2 < total) load(q + 2, rc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int b = PB - 1; b >= 0; --b)
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          const uint4 fb = *reinterpret_cast<const uint4 *>(&lb[r][b][lds_at(wn + j * 16 + lr, h * 32 + lg * 8)]);
+#pragma unroll
+          for (int p = PA - 1; p >= 0; --p)
+            if (p + b < kPieces)
+#pragma unroll
+              for (int i = 0; i < S; ++i)
+                acc[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, fa[s][h][p][i]), acc[i][j]);
+        }
+    if (q + 1 < total) store(q + 1, next);
+    if (s == KS - 1) {  // the column tile is complete
+      const int n0 = (nt0 + q / KS) * kTile;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const int m = m0 + wm + i * 16 + lr;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          const int n = n0 + wn + j * 16 + 4 * lg;  // N is a multiple of 8
+          if (m < g.a.rows && n < N)
+            *reinterpret_cast<float4 *>(g.out + int64_t(m) * N + n) =
+                make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        }
+      }
+      clear();
+    }
+    __syncthreads();
+  };
+  using R0 = std::integral_constant<int, 0>;
+  using R1 = std::integral_constant<int, 1>;
+  clear();
+  load(0, R0{});
+  load(min(1, total - 1), R1{});
+  store(0, R0{});
+  __syncthreads();
+  int q = 0;
+  for (; q + 1 < total; q += 2) {
+    step(q, R0{}, R1{});
+    step(q + 1, R1{}, R0{});
+  }
+  if (q < total) step(q, R0{}, R1{});
+}
+
 // ---- rows of logits ---------------------------------------------------------
 
 // Sequence of token t: the last b with off[b] <= t (0 without offsets), kept
@@ -945,6 +1039,16 @@ void launch_gemm(GemmArgs g, int parts, hipStream_t s, bool sums_only = false) {
   }
 }
 
+// Column tiles per workgroup: as many as leave two workgroups for each CU.
+template <int DT, int KS>
+void launch_dx(const GemmArgs &g, hipStream_t s) {
+  const int64_t mt = tiles_of(g.a.rows);
+  const int nt = tiles_of(g.b.rows), per = int(std::max<int64_t>(1, std::min<int64_t>(nt, mt * nt / 512)));
+  const dim3 grid(unsigned((nt + per - 1) / per), unsigned(mt));
+  if (g.b.vec) launch((balance_dx_kernel<DT, true, KS>), grid, dim3(kThreads), 0, s, g, per);
+  else launch((balance_dx_kernel<DT, false, KS>), grid, dim3(kThreads), 0, s, g, per);
+}
+
 template <typename F>
 void by_experts(int E, F &&f) {
   if (E <= 64) f(std::integral_constant<int, 1>{});
@@ -1069,7 +1173,10 @@ void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, 
       g.b = Operand{w_router, E, D, E % (16 / esz) == 0};
       g.K = E, g.out = dx;
       by_dtype(d->act_dtype, [&](auto dt) {
-        launch_gemm<kDtPieces, true, decltype(dt)::value, true, false, false>(g, 1, s);
+        constexpr int DT = decltype(dt)::value;
+        if (E <= kStep) launch_dx<DT, 1>(g, s);
+        else if (E <= 2 * kStep) launch_dx<DT, 2>(g, s);
+        else launch_gemm<kDtPieces, true, DT, true, false, false>(g, 1, s);
       });
     }
   }
