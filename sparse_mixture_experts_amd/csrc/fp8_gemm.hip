@@ -58,12 +58,25 @@ __device__ __forceinline__ uint32_t piece_at(int m, int c) { return uint32_t(m *
 // A wave's 1 KB covers 8 rows; the piece that lane l brings for its place.
 __device__ __forceinline__ int piece_of_lane(int l) { return (l % kPieces) ^ (l / kPieces); }
 
+// Two weight tiles hold 32 rows in turn by fours: row r of tile nt is row
+// 8 (r / 4) + 4 (nt % 2) + r % 4 of the pair's, so that a lane's results of
+// the two are 8 neighbouring outputs: 16 bytes of 16-bit ones, 64 a row and
+// store, where single tiles wrote 8 and 32 (8192 x 5632 x 2048: 125 us, 115
+// with pairs).  pair_key: the exchange of a row's pieces in LDS that keeps
+// reads in this order on different banks.
+__device__ __forceinline__ int pair_row(int nt, int r) { return nt / 2 * 32 + 8 * (r / 4) + 4 * (nt % 2) + r % 4; }
+__device__ __forceinline__ int pair_key(int m) { return (m & 3) | ((m >> 3) & 1) << 2; }
+
 // One 16 x 128 tile of weight codes on its way from memory to the operand
 // layout.  Loaded as it lies in memory (8 lanes to the 128 bytes of a row, so
 // that an instruction meets 8 cache lines; in the operand's own layout
 // neighbouring lanes are in different rows, and each load met 64), it is
 // turned around through a piece of LDS that only this wave uses.
 constexpr int kTileBytes = 16 * kFp8Block;
+template <bool PAIR>
+__device__ __forceinline__ uint32_t weight_at(int m, int c) {
+  return PAIR ? uint32_t(m * kFp8Block + (c ^ pair_key(m)) * 16) : piece_at(m, c);
+}
 struct WeightTile {
   uint4 v[2];
   // base: the tile's first row; k0: the block's first code.  Past the end of
@@ -74,17 +87,21 @@ struct WeightTile {
     v[0] = *reinterpret_cast<const uint4 *>(base + o);
     v[1] = *reinterpret_cast<const uint4 *>(base + 8 * int64_t(K) + o);
   }
+  // PAIR: for reads in the order of pair_row
+  template <bool PAIR = false>
   __device__ __forceinline__ void put(uint8_t *lds, int K, int k0) const {
     const int lane = lane_id(), m = lane / kPieces, c = lane % kPieces;
     const bool ok = k0 + c * 16 < K;
-    *reinterpret_cast<uint4 *>(lds + piece_at(m, c)) = keep(v[0], ok);
-    *reinterpret_cast<uint4 *>(lds + piece_at(m + 8, c)) = keep(v[1], ok);
+    *reinterpret_cast<uint4 *>(lds + weight_at<PAIR>(m, c)) = keep(v[0], ok);
+    *reinterpret_cast<uint4 *>(lds + weight_at<PAIR>(m + 8, c)) = keep(v[1], ok);
   }
 };
-__device__ __forceinline__ i32x8 tile_operand(const uint8_t *lds) {
-  const int lr = lane_id() & 15, lg = lane_id() >> 4;
-  return join8(*reinterpret_cast<const uint4 *>(lds + piece_at(lr, lg)),
-               *reinterpret_cast<const uint4 *>(lds + piece_at(lr, lg + 4)));
+// Tile nt of those that follow one another in `lds`.
+template <bool PAIR = false>
+__device__ __forceinline__ i32x8 tile_operand(const uint8_t *lds, int nt) {
+  const int lr = lane_id() & 15, lg = lane_id() >> 4, m = PAIR ? pair_row(nt, lr) : nt * 16 + lr;
+  return join8(*reinterpret_cast<const uint4 *>(lds + weight_at<PAIR>(m, lg)),
+               *reinterpret_cast<const uint4 *>(lds + weight_at<PAIR>(m, lg + 4)));
 }
 
 // What a projection writes: the product, or the gated unit of two of them
@@ -224,6 +241,18 @@ __device__ __forceinline__ void store4(const Fp8Args &a, int64_t at, const fp8_a
   }
 }
 
+// Eight consecutive outputs of one row, 16 bits each.
+__device__ __forceinline__ void store8(const Fp8Args &a, int64_t at, const fp8_acc &u, const fp8_acc &v) {
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = a.out_dtype == MOE_DT_F16 ? f32_to_f16_bits(u[i]) : f32_to_bf16_bits(u[i]);
+    h[4 + i] = a.out_dtype == MOE_DT_F16 ? f32_to_f16_bits(v[i]) : f32_to_bf16_bits(v[i]);
+  }
+  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) =
+      make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
 // The tile of 16 RB token rows (32, 48 or 64) by 256 weight rows.  Weights
 // and rows are requested two blocks ahead of their use, into two sets of
 // registers: with one block in flight a workgroup waited out a memory round
@@ -249,6 +278,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args &a, const PlanItem &tile
                                           Turn &turn, typename TileLds<RB, EXACT>::Scales &ss,
                                           typename TileLds<RB, EXACT>::Max &rmax) {
   constexpr int BM = TileLds<RB, EXACT>::BM, XB = TileLds<RB, EXACT>::XB, NSL = TileLds<RB, EXACT>::NSL;
+  constexpr bool PAIR = MODE == kPlain && !EXACT;   // (16-bit results)
   constexpr int NP = 2;                             // weight tiles that a read of the rows serves
   constexpr int PPT = BM * kPieces / kThreads;      // 16-byte pieces of the rows per thread
   constexpr int NTH = MODE == kGated ? kNT / 2 : kNT;
@@ -341,7 +371,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args &a, const PlanItem &tile
   auto step = [&](int s, auto rc) {
     constexpr int r = decltype(rc)::value;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) wq[r][nt].put(turn[wave][nt], K, s * kFp8Block);
+    for (int nt = 0; nt < kNT; ++nt) wq[r][nt].template put<PAIR>(turn[wave][nt], K, s * kFp8Block);
     // (the loads stay behind the last use of the registers that they fill)
     __builtin_amdgcn_sched_barrier(0);
     load_rows(s + 2, r);
@@ -349,7 +379,7 @@ __device__ __forceinline__ void tile_body(const Fp8Args &a, const PlanItem &tile
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int np = 0; np < kNT; np += NP) {
-      const Fp8Operand<EXACT> w0(tile_operand(turn[wave][np])), w1(tile_operand(turn[wave][np + NP - 1]));
+      const Fp8Operand<EXACT> w0(tile_operand<PAIR>(turn[wave][0], np)), w1(tile_operand<PAIR>(turn[wave][0], np + NP - 1));
 #pragma unroll
       for (int mt = 0; mt < RB; ++mt) {
         const uint4 *row = reinterpret_cast<const uint4 *>(&sa[r][mt * 16 + lr][lg * 16 * XB]);
@@ -394,11 +424,18 @@ __device__ __forceinline__ void tile_body(const Fp8Args &a, const PlanItem &tile
       if (m < tile.rows) {
         // (codes of zero are not enough where a weight is a NaN)
         const bool ok = source_row(a, tile.row0 + m) >= 0;
-        const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
+        const fp8_acc z = {0.f, 0.f, 0.f, 0.f};
+        const int64_t at = int64_t(tile.row0 + m) * a.N + col0;
+        if constexpr (PAIR) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-          if (col0 + nt * 16 < a.N)
-            store4(a, at + col0 + nt * 16, ok ? acc[nt][mt] : fp8_acc{0.f, 0.f, 0.f, 0.f});
+          for (int nt = 0; nt < kNT; nt += 2)
+            if (col0 + nt * 16 + 8 * lg < a.N)
+              store8(a, at + nt * 16 + 8 * lg, ok ? acc[nt][mt] : z, ok ? acc[nt + 1][mt] : z);
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+            if (col0 + nt * 16 < a.N) store4(a, at + nt * 16 + 4 * lg, ok ? acc[nt][mt] : z);
+        }
       }
     }
   } else {
@@ -462,7 +499,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_tile_kernel(Fp8Args a) {
 // 32 cycles for 16 KB read from LDS and 8 KB from memory, so that with two
 // waves per SIMD neither path (128 and 64 bytes a cycle) is near its limit.
 // The rows go from memory to LDS without passing through registers.  4096
-// rows, N = 4096, K = 2048: 51 us, 1.35 PFLOP/s (the tile kernel 66).  Neither
+// rows, N = 4096, K = 2048: 50 us, 1.36 PFLOP/s (the tile kernel 66).  Neither
 // memory, LDS nor the fmas alone bound it: left out one by one in timing
 // copies, each changed it by a few percent.  What is left are the waits of
 // two workgroups per CU at one barrier per block.
@@ -513,9 +550,9 @@ __device__ __forceinline__ void wide_body(const Fp8Args &a, const PlanItem &tile
   auto stage = [&](int s, float (&ss)[2][BM]) {  // block s: scales to LDS, weights through it
     ss[sn][sm] = srow >= 0 ? sga * sgw : 0.f;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) wn[nt].put(turn[wave][nt], K, s * kFp8Block);
+    for (int nt = 0; nt < kNT; ++nt) wn[nt].template put<true>(turn[wave][nt], K, s * kFp8Block);
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) w[nt] = tile_operand(turn[wave][nt]);
+    for (int nt = 0; nt < kNT; ++nt) w[nt] = tile_operand<true>(turn[wave][0], nt);
   };
   fp8_acc acc[kNT][RB];
 #pragma unroll
@@ -580,11 +617,11 @@ __device__ __forceinline__ void wide_body(const Fp8Args &a, const PlanItem &tile
     const int m = mt * 16 + lr;
     if (m < tile.rows) {
       const bool ok = source_row(a, tile.row0 + m) >= 0;
-      const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
+      const int64_t at = int64_t(tile.row0 + m) * a.N + 8 * lg + col0;
+      const fp8_acc z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-        if (col0 + nt * 16 < a.N)
-          store4(a, at + col0 + nt * 16, ok ? acc[nt][mt] : fp8_acc{0.f, 0.f, 0.f, 0.f});
+      for (int nt = 0; nt < kNT; nt += 2)
+        if (col0 + nt * 16 + 8 * lg < a.N) store8(a, at + nt * 16, ok ? acc[nt][mt] : z, ok ? acc[nt + 1][mt] : z);
     }
   }
 }
@@ -631,7 +668,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_mixed_kernel(Fp8Args a) {
 // The 256-row tile, for large products: 8 waves of 128 token rows by 64
 // weight rows, both operands from memory to LDS without passing through
 // registers and read from there as they are used (24 KB for a wave's 32
-// products).  One workgroup fills a CU.  8192 x 5632 x 2048: 122 us, 1.55
+// products).  One workgroup fills a CU.  8192 x 5632 x 2048: 115 us, 1.65
 // PFLOP/s; the instruction alone, fed from registers with random codes,
 // reaches 3.7, and a bf16 product of the library 1.2.
 constexpr int kHugeRows = 256;
@@ -653,7 +690,7 @@ __global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
   const int col0 = bx * kBN + wave * kNT * 16, m0 = wave_id / kNW * RB * 16;
   const int nbr = (a.N + kFp8Block - 1) / kFp8Block;
   // pass p of either operand: row 64 p + tid / 8, the piece that belongs at place tid % 8
-  const int piece = piece_of_lane(lane);
+  const int piece = piece_of_lane(lane), piece_w = lane % kPieces ^ pair_key(tid / kPieces);
   const uint8_t *ap[PASS];
   uint32_t wo[PASS];  // rows of the tile's columns, from the first one's weights
   const uint8_t *wbase = a.w0 + (int64_t(tile.expert) * a.N + bx * kBN) * K;
@@ -672,12 +709,12 @@ __global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
   float sga, sgw;
   auto load = [&](int s, uint8_t *ba, uint8_t *bw) {
     s = min(s, nb - 1);
-    const int k = min(s * kFp8Block + piece * 16, K - 16);
+    const int k = min(s * kFp8Block + piece * 16, K - 16), kw = min(s * kFp8Block + piece_w * 16, K - 16);
 #pragma unroll
     for (int p = 0; p < PASS; ++p) {
       const int at = (p * (kHugeThreads / kWave) + wave_id) * (kWave * 16);
       to_lds(ap[p] + k, ba + at);
-      to_lds(wbase + (wo[p] + uint32_t(k)), bw + at);
+      to_lds(wbase + (wo[p] + uint32_t(kw)), bw + at);
     }
     sga = sap[int64_t(s) * a.a_rows];
     sgw = swp[s];
@@ -699,8 +736,13 @@ __global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
       const uint4 hi = *reinterpret_cast<const uint4 *>(b + row * kFp8Block + r1);
       return Fp8Operand<false>(TAIL ? join8(keep(lo, ok0), keep(hi, ok1)) : join8(lo, hi));
     };
-    const Fp8Operand<false> w[kNT] = {read(bw, wave * 64), read(bw, wave * 64 + 16), read(bw, wave * 64 + 32),
-                                      read(bw, wave * 64 + 48)};
+    auto read_w = [&](int nt) {
+      const int m = wave * 64 + pair_row(nt, lr);
+      const uint4 lo = *reinterpret_cast<const uint4 *>(bw + m * kFp8Block + (lg ^ pair_key(m)) * 16);
+      const uint4 hi = *reinterpret_cast<const uint4 *>(bw + m * kFp8Block + ((lg + 4) ^ pair_key(m)) * 16);
+      return Fp8Operand<false>(TAIL ? join8(keep(lo, ok0), keep(hi, ok1)) : join8(lo, hi));
+    };
+    const Fp8Operand<false> w[kNT] = {read_w(0), read_w(1), read_w(2), read_w(3)};
     Fp8Operand<false> x = read(ba, m0);
     float sc = ss[wave / 2][m0 + lr];
 #pragma unroll
@@ -746,11 +788,11 @@ __global__ __launch_bounds__(kHugeThreads, 2) void fp8_huge_kernel(Fp8Args a) {
     const int m = m0 + mt * 16 + lr;
     if (m < tile.rows) {
       const bool ok = source_row(a, tile.row0 + m) >= 0;
-      const int64_t at = int64_t(tile.row0 + m) * a.N + 4 * lg;
+      const int64_t at = int64_t(tile.row0 + m) * a.N + 8 * lg + col0;
+      const fp8_acc z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-        if (col0 + nt * 16 < a.N)
-          store4(a, at + col0 + nt * 16, ok ? acc[nt][mt] : fp8_acc{0.f, 0.f, 0.f, 0.f});
+      for (int nt = 0; nt < kNT; nt += 2)
+        if (col0 + nt * 16 + 8 * lg < a.N) store8(a, at + nt * 16, ok ? acc[nt][mt] : z, ok ? acc[nt + 1][mt] : z);
     }
   }
 }
@@ -827,7 +869,7 @@ __global__ __launch_bounds__(kThreads, 2) void fp8_decode_kernel(Fp8Args a) {
     const float sxv = rok ? sx[d] : 0.f;
 #pragma unroll
     for (int nt = 0; nt < WN; ++nt) {
-      const fp8_acc v = fp8_product(Fp8Operand<true>(tile_operand(turn[wave][nt])), xo);
+      const fp8_acc v = fp8_product(Fp8Operand<true>(tile_operand(turn[wave][0], nt)), xo);
       const float sc = sxv * sq[d][nt];
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[nt][i] = __builtin_fmaf(v[i], sc, acc[nt][i]);
