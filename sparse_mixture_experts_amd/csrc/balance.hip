@@ -318,9 +318,9 @@ struct Stage<kDtPieces, KC, false, true> {
 // Bound by latency more than by either rate: a step is one round through LDS
 // and 8 to 48 matrix instructions a wave, with two or three workgroups per CU
 // to hide it.  2048 tokens, d_model 2048, 512 experts (bf16): logits 18.3 us
-// for 4.3 GFLOP and 10.5 MB read; 8192 tokens, 128 experts: dx 34 us and dW
-// 39 us for 12.9 GFLOP each in matrix-core products.  Tiles of 128 x 128
-// spilled with three pieces, and 4 waves per SIMD spilled too (both slower).
+// for 4.3 GFLOP and 10.5 MB read; 8192 tokens, 128 experts: dW 37 us for 12.9
+// GFLOP in matrix-core products.  Tiles of 128 x 128 spilled with three
+// pieces, and 4 waves per SIMD spilled too (both slower).
 template <int DTA, bool KCA, int DTB, bool KCB, bool NATIVE, bool MASK, bool VECB>
 __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
   using SA = Stage<DTA, KCA, NATIVE, true>;
@@ -328,7 +328,8 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
   constexpr int PA = SA::P, PB = SB::P, S = 2;
   // Two buffers (one barrier a step, a step's elements stored while the last
   // one's are multiplied) for single pieces; with more, the second one costs
-  // occupancy (8192 tokens, 128 experts, dx: 34 us with one, 39 with two).
+  // occupancy (8192 tokens, 128 experts, dx by this kernel: 34 us with one,
+  // 39 with two).
   constexpr int BUF = PA + PB <= 2 ? 2 : 1;
   __shared__ __align__(16) uint16_t la[BUF][PA][kTile * kStep], lb[BUF][PB][kTile * kStep];
   const int lane = lane_id(), wave = threadIdx.x / kWave, lr = lane & 15, lg = lane >> 4;
@@ -465,7 +466,9 @@ __global__ __launch_bounds__(kThreads, 2) void split_gemm_kernel(GemmArgs g) {
 // dx = dl W^T for at most 64 KS experts: a workgroup keeps the pieces of its 64
 // tokens' dl in registers, as operands, and runs over column tiles of W, two
 // steps ahead (a reduction this short is over before a workgroup of its own
-// for every 64 x 64 results has its operands).
+// for every 64 x 64 results has its operands).  Bound by the results: 8192
+// tokens, 128 experts, d_model 2048 (67 MB) 23 us; 29 with ordinary stores,
+// and 34 with a workgroup for each tile.
 template <int DT, bool VECB, int KS>
 __global__ __launch_bounds__(kThreads, 2) void balance_dx_kernel(GemmArgs g, int per_wg) {
   using SB = Stage<DT, true, false, VECB>;
@@ -533,8 +536,7 @@ __global__ __launch_bounds__(kThreads, 2) void balance_dx_kernel(GemmArgs g, int
         for (int j = 0; j < S; ++j) {
           const int n = n0 + wn + j * 16 + 4 * lg;  // N is a multiple of 8
           if (m < g.a.rows && n < N)
-            *reinterpret_cast<float4 *>(g.out + int64_t(m) * N + n) =
-                make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+            __builtin_nontemporal_store(acc[i][j], reinterpret_cast<f32x4 *>(g.out + int64_t(m) * N + n));
         }
       }
       clear();

@@ -5,8 +5,8 @@
 // Both kernels read their input once and hold it in registers between the
 // maximum and the rounding, so they are bound by memory: an element costs its
 // own bytes and one byte of code.  Matrices of 128 x 1536 x 2048 bf16 values
-// (0.81 GB read, 0.40 GB written): 230 us, 5.25 TB/s, what a large copy
-// reaches.  32 rows of 2048: 5 us, a launch and one memory round trip.
+// (0.81 GB read, 0.40 GB written): 221 us, 5.45 TB/s (a large copy
+// reaches 5.1).  32 rows of 2048: 5 us, a launch and one memory round trip.
 #include "fp8_common.h"
 #include "launch.h"
 #include "moe_internal.h"
@@ -48,11 +48,16 @@ __device__ __forceinline__ float absmax16(const float (&v)[kPer]) {
   return m;
 }
 
+// PASSING: codes that nothing reads soon (a loaded layer's weights) do not
+// displace what the L2 holds: 221 us instead of 230.
+template <bool PASSING>
 __device__ __forceinline__ void store16(uint8_t *p, const float (&v)[kPer], const Fp8Quant &q) {
-  uint32_t w[4];
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 w;
 #pragma unroll
   for (int u = 0; u < 4; ++u) w[u] = fp8_pack4(q(v[4 * u]), q(v[4 * u + 1]), q(v[4 * u + 2]), q(v[4 * u + 3]));
-  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (PASSING) __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
+  else *reinterpret_cast<u32x4 *>(p) = w;
 }
 
 // A workgroup takes 32 rows of one column block (their scales are then one
@@ -69,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(const void *x, int r
   const int64_t at = int64_t(r) * cols + c;
   if (c < cols) load16<DT>(x, at, v);  // cols is a multiple of 16
   const Fp8Quant q(max8_lanes(absmax16(v)));
-  if (c < cols) store16(codes + at, v, q);
+  if (c < cols) store16<false>(codes + at, v, q);
   if (threadIdx.x % kLanes == 0) scales[int64_t(j) * rows + r] = q.scale;
 }
 
@@ -103,7 +108,7 @@ __global__ __launch_bounds__(kThreads) void fp8_blocks_kernel(const void *x, int
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
     const int r = r0 + p * kRowsPass;
-    if (r < rows && c < cols) store16(codes + base + int64_t(r) * cols + c, v[p], q);
+    if (r < rows && c < cols) store16<true>(codes + base + int64_t(r) * cols + c, v[p], q);
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = q.scale;
 }
