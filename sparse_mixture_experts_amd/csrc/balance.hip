@@ -596,32 +596,35 @@ struct RowArgs {
   int ld;
 };
 
-constexpr int kRowWaves = kThreads / kWave;
-constexpr int kPair = 2;  // tokens that a wave takes at a time, all their loads in flight together
+// Waves of the row kernels, and tokens that a wave takes at a time: eight
+// tokens as 8 x 1 instead of 4 x 2 took the forward rows of 2048 tokens and
+// 512 experts from 11.8 to 8.9 us, the backward rows of 256 from 5.2 to 4.3
+// (of 8192, 128 experts, 8.7 to 9.1).
+constexpr int kRowWaves = 8, kPair = 1;
 
-// Experts lane, lane + 64, ... of the logits of tokens t and t + 1 (up to
-// t1 - 1); -inf past the end.  Partial logits are summed in their order.
-template <int EPL>
-__device__ __forceinline__ void load_rows(const RowArgs &a, int t, int t1, float (&l)[kPair][EPL]) {
+// Experts lane, lane + 64, ... of the logits of PAIR tokens from t on (up to
+// t1 - 1), all their loads in flight together; -inf past the end.  Partial logits are summed in their order.
+template <int EPL, int PAIR>
+__device__ __forceinline__ void load_rows(const RowArgs &a, int t, int t1, float (&l)[PAIR][EPL]) {
   const int lane = lane_id();
   const int64_t part = int64_t(a.tokens.T) * a.E;
   const float *src = a.parts ? a.parts : a.logits;
   const int nz = a.parts ? a.z : 1;
 #pragma unroll
-  for (int q = 0; q < kPair; ++q)
+  for (int q = 0; q < PAIR; ++q)
 #pragma unroll
     for (int i = 0; i < EPL; ++i) l[q][i] = a.parts && a.bias ? a.bias[min(lane + kWave * i, a.E - 1)] : 0.f;
   // (the bias first: its place in the sum is free, its loads are not waited for)
 #pragma unroll 2
   for (int z = 0; z < nz; ++z)
 #pragma unroll
-    for (int q = 0; q < kPair; ++q)
+    for (int q = 0; q < PAIR; ++q)
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
         l[q][i] += src[z * part + int64_t(min(t + q, t1 - 1)) * a.E + min(lane + kWave * i, a.E - 1)];
   if (a.parts) {
 #pragma unroll
-    for (int q = 0; q < kPair; ++q)
+    for (int q = 0; q < PAIR; ++q)
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = lane + kWave * i;
@@ -629,7 +632,7 @@ __device__ __forceinline__ void load_rows(const RowArgs &a, int t, int t1, float
       }
   }
 #pragma unroll
-  for (int q = 0; q < kPair; ++q)
+  for (int q = 0; q < PAIR; ++q)
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (lane + kWave * i >= a.E) l[q][i] = -INFINITY;
@@ -669,13 +672,13 @@ __device__ __forceinline__ void count_row(const RowArgs &a, float (&l)[EPL], int
 // Forward: a workgroup takes a chunk of consecutive tokens, 8 at a time, and
 // leaves, for every sequence among them, the sums of its counted tokens'
 // probabilities and the counts of their slots, at place chunk number +
-// sequence number (which no other pair shares).  A wave's two rows are
+// sequence number (which no other pair shares).  A wave's row is
 // requested before the tokens' sequence is looked up.  2048 tokens and 512
-// experts: 11.9 us for 8 MB of partial logits read and 4 MB written, a chain
+// experts: 8.9 us for 8 MB of partial logits read and 4 MB written, a chain
 // of three memory round trips (rows, the sequence table, records) and the
 // exponentials; a 4-fold split of the logits' reduction made this kernel 40 us.
 template <int EPL>
-__global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
+__global__ __launch_bounds__(kRowWaves * kWave) void balance_rows_kernel(RowArgs a) {
   __shared__ float ps[kRowWaves][EPL * kWave];
   __shared__ int32_t cs[kRowWaves][EPL * kWave], ns[kRowWaves];
   const int c0 = int(blockIdx.x) * a.chunk, c1 = min(c0 + a.chunk, a.tokens.T);
@@ -694,7 +697,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
     if (lane == 0) ns[wave] = n;
     __syncthreads();
     const int64_t at = int64_t(blockIdx.x) + b;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    for (int e = threadIdx.x; e < a.E; e += kRowWaves * kWave) {
       float p = ps[0][e];
       int32_t c = cs[0][e];
 #pragma unroll
@@ -702,7 +705,12 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
       a.psum[at * a.E + e] = p;
       a.count[at * a.E + e] = c;
     }
-    if (threadIdx.x == 0) a.ntok[at] = ns[0] + ns[1] + ns[2] + ns[3];
+    if (threadIdx.x == 0) {
+      int32_t all = ns[0];
+#pragma unroll
+      for (int w = 1; w < kRowWaves; ++w) all += ns[w];
+      a.ntok[at] = all;
+    }
     __syncthreads();
     reset();
   };
@@ -719,7 +727,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(RowArgs a) {
       slot[q] = a.idx[int64_t(t) * a.K + min(lane, a.K - 1)];  // slot j in lane j
       on[q] = !a.tokens.mask || a.tokens.mask[t];
     }
-    load_rows<EPL>(a, tw, c1, l);
+    load_rows<EPL, kPair>(a, tw, c1, l);
     int lo, hi;
     token_range(a.tokens, lo, hi);
     int t0 = max(c, lo);
@@ -816,9 +824,9 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(FinishAr
 }
 
 // Backward of the rows: dl of a chunk of tokens, cut into its three planes
-// (8192 tokens, 128 experts: 9.2 us for 4.2 MB read and 6.3 MB written).
+// (8192 tokens, 128 experts: 9.1 us for 4.2 MB read and 6.3 MB written).
 template <int EPL>
-__global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
+__global__ __launch_bounds__(kRowWaves * kWave) void balance_dlogits_kernel(RowArgs a) {
   const int c0 = int(blockIdx.x) * a.chunk, c1 = min(c0 + a.chunk, a.tokens.T);
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   int lo, hi;
@@ -842,7 +850,7 @@ __global__ __launch_bounds__(kThreads) void balance_dlogits_kernel(RowArgs a) {
       dws[q] = a.dtopk ? a.dtopk[at] : 0.f;
       if (lane >= a.K || unsigned(slots[q]) >= unsigned(a.E)) slots[q] = -1;
     }
-    load_rows<EPL>(a, t, c1, l);
+    load_rows<EPL, kPair>(a, t, c1, l);
 #pragma unroll
     for (int q = 0; q < kPair; ++q)
       lsel[q] = a.dtopk ? a.logits[int64_t(min(t + q, c1 - 1)) * a.E + max(slots[q], 0)] : 0.f;
@@ -935,7 +943,7 @@ __global__ __launch_bounds__(kThreads) void sum_parts_kernel(const float *p, int
 // The whole reduction of a small call in one workgroup: rows, sums over each
 // sequence's tokens and the loss, instead of further launches that cost more
 // than their work (16 tokens, 8 experts: the call 8 us instead of 12.8).
-constexpr int kSmallWaves = 8, kSmallTokens = 32, kSmallSeqs = 8;
+constexpr int kSmallWaves = 8, kSmallPair = 2, kSmallTokens = 32, kSmallSeqs = 8;
 template <int EPL>
 __global__ __launch_bounds__(kSmallWaves *kWave) void balance_small_kernel(RowArgs a, FinishArgs f) {
   __shared__ float ps[kSmallWaves][EPL * kWave], ls[kSmallWaves];
@@ -944,10 +952,10 @@ __global__ __launch_bounds__(kSmallWaves *kWave) void balance_small_kernel(RowAr
   const int T = a.tokens.T;
   int lo, hi;
   token_range(a.tokens, lo, hi);
-  float l[kPair][EPL];
+  float l[kSmallPair][EPL];
   if (a.parts) {  // tokens of no sequence: their logits alone
-    for (int t = kPair * wave; t < lo; t += kPair * kSmallWaves) load_rows<EPL>(a, t, lo, l);
-    for (int t = hi + kPair * wave; t < T; t += kPair * kSmallWaves) load_rows<EPL>(a, t, T, l);
+    for (int t = kSmallPair * wave; t < lo; t += kSmallPair * kSmallWaves) load_rows<EPL, kSmallPair>(a, t, lo, l);
+    for (int t = hi + kSmallPair * wave; t < T; t += kSmallPair * kSmallWaves) load_rows<EPL, kSmallPair>(a, t, T, l);
   }
   float loss = 0.f;
   int filled = 0;
@@ -961,13 +969,13 @@ __global__ __launch_bounds__(kSmallWaves *kWave) void balance_small_kernel(RowAr
     int32_t cnt[EPL], n = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sum[i] = 0.f, cnt[i] = 0;
-    for (int t = t0 + kPair * wave; t < t1; t += kPair * kSmallWaves) {
-      int slot[kPair];
+    for (int t = t0 + kSmallPair * wave; t < t1; t += kSmallPair * kSmallWaves) {
+      int slot[kSmallPair];
 #pragma unroll
-      for (int q = 0; q < kPair; ++q) slot[q] = a.idx[int64_t(min(t + q, t1 - 1)) * a.K + min(lane, a.K - 1)];
-      load_rows<EPL>(a, t, t1, l);
+      for (int q = 0; q < kSmallPair; ++q) slot[q] = a.idx[int64_t(min(t + q, t1 - 1)) * a.K + min(lane, a.K - 1)];
+      load_rows<EPL, kSmallPair>(a, t, t1, l);
 #pragma unroll
-      for (int q = 0; q < kPair; ++q)
+      for (int q = 0; q < kSmallPair; ++q)
         if (t + q < t1 && (!a.tokens.mask || a.tokens.mask[t + q])) count_row<EPL>(a, l[q], slot[q], sum, cnt, n);
     }
 #pragma unroll
@@ -1003,7 +1011,7 @@ __global__ __launch_bounds__(kSmallWaves *kWave) void balance_small_kernel(RowAr
   }
 }
 
-// Tokens per workgroup of the row kernels: 8 (two for each wave), more where
+// Tokens per workgroup of the row kernels: 8 (one for each wave), more where
 // the chunks would be many more than the GPU takes at once.
 int chunk_tokens(int32_t T) { return T <= 8192 ? 8 : T <= 65536 ? 32 : 128; }
 int chunks_of(int32_t T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
@@ -1141,7 +1149,7 @@ void launch_balance_loss(const moe_layer_desc *d, int32_t T, const void *x, cons
     return;
   }
   by_experts(E, [&](auto n) {  // (without tokens: for the ticket alone)
-    launch((balance_rows_kernel<decltype(n)::value>), dim3(std::max(1, chunks_of(T))), dim3(kThreads), 0, s, r);
+    launch((balance_rows_kernel<decltype(n)::value>), dim3(std::max(1, chunks_of(T))), dim3(kRowWaves * kWave), 0, s, r);
   });
   FinishArgs f{tk, E, d->top_k, chunk_tokens(T), at<float>(ws, L.psum), at<int32_t>(ws, L.count), at<int32_t>(ws, L.ntok),
                counts, seq_tokens, mean, at<float>(ws, L.terms), at<int32_t>(ws, L.ticket), loss};
@@ -1166,7 +1174,7 @@ void launch_balance_backward(const moe_layer_desc *d, int32_t T, const void *x, 
     r.counts = counts, r.seq_tokens = seq_tokens, r.dloss = dloss, r.dtopk = dtopk_w, r.renorm = d->renormalize;
     r.dl = at<uint16_t>(ws, L.dl), r.ld = L.ld;
     by_experts(E, [&](auto n) {
-      launch((balance_dlogits_kernel<decltype(n)::value>), dim3(chunks_of(T)), dim3(kThreads), 0, s, r);
+      launch((balance_dlogits_kernel<decltype(n)::value>), dim3(chunks_of(T)), dim3(kRowWaves * kWave), 0, s, r);
     });
     if (dx) {
       GemmArgs g{};
